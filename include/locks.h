@@ -111,6 +111,13 @@ typedef enum {
 #define LOCKS_RECORD_BYTES 832
 #define LOCKS_RECORD_PAYLOAD_BYTES 818
 #define LOCKS_UNQUANTISED_FLOATS 1296 /* 16 + 128 + 128*8 + 16*8 */
+#define LOCKS_KV_RECORD_BYTES 4128    /* quantised cache, see below */
+
+/* element types of the rows that the quantised cache is written from and
+ * read back as */
+#define LOCKS_TYPE_BF16 0
+#define LOCKS_TYPE_FP16 1
+#define LOCKS_TYPE_FP32 2
 
 /* Human-readable name of a status code (static string). */
 const char *locks_status_string(locks_status_t s);
@@ -128,8 +135,9 @@ long long locks_kernel_launches(void);
 /* Bytes per summary record (832: 818 B payload + 14 B padding). */
 size_t locks_summary_record_bytes(void);
 
-/* Workspace bytes needed by locks_score_select, locks_select_pages and
- * locks_sparse_decode for these sizes (k = max_pages covers dense decode).
+/* Workspace bytes needed by locks_score_select, locks_select_pages,
+ * locks_sparse_decode and locks_quantised_decode for these sizes (k =
+ * max_pages covers dense decode).
  * One workspace may serve those calls in stream order.  Its first int32 is
  * the device status word: clear it once (locks_clear_status) before use. */
 locks_status_t locks_workspace_size(int batch, int h_q, int h_kv,
@@ -468,6 +476,119 @@ int locks_decoder_last_cuda_error(const locks_decoder_t *decoder);
 /* Release the decoder's graph, stream and host word (NULL is a no-op).
  * The caller's buffers are untouched. */
 void locks_decoder_destroy(locks_decoder_t *decoder);
+
+/* ------------------------------------------------------------------------
+ * Quantised KV cache: keys and values in 8 bits, half the bytes of the bf16
+ * cache to hold and to read.  The pages describe no such cache (their
+ * decode reads K/V as the engine keeps it); it stands beside the bf16 calls
+ * and uses the same page tables, lengths, selections and status bits.
+ *
+ * The cache is an array of records [num_phys_pages][h_kv], 16-byte aligned,
+ * LOCKS_KV_RECORD_BYTES (4128) each, one per (page, KV head):
+ *   [   0, 2048)  e4m3 codes of the page's 16 key rows, 128 bytes a row
+ *   [2048, 4096)  e4m3 codes of its 16 value rows
+ *   [4096, 4112)  the key rows' scale exponents, byte e + 127 for 2^e
+ *   [4112, 4128)  the value rows' scale exponents
+ * e4m3: sign, 4 exponent bits of bias 7, 3 fraction bits, largest 448, no
+ * infinities, 0x7f/0xff not a number.  Dims 16c .. 16c + 15 of the row in
+ * slot s (s = position % 16) are the 16 bytes at
+ * 128 s + 16 (c ^ (s & 6) ^ 5 (s & 1)), which lets the attention kernels
+ * read rows and columns without shared-memory bank conflicts.
+ *
+ * A row x of 128 numbers is kept with the least e such that
+ * max |x| <= 448 * 2^e, limited to -32 <= e <= 31, as codes
+ * e4m3(x / 2^e), round to nearest even, clamped to +-448; a number's error
+ * is at most 2^-4 of it, or 2^(e-10) where that is more.  The division is
+ * exact, so every platform finds the same codes.  Infinities, and magnitudes above 448 * 2^31,
+ * become +-448 * 2^31; NaN stays NaN and has no part in the maximum; rows
+ * below 448 * 2^-32 keep e = -32 and lose low bits.  A number read back,
+ * code * 2^e, is exact in bf16 and fp32.
+ * ------------------------------------------------------------------------ */
+
+/* Write rows of new tokens (a prompt's, or one per sequence) into the
+ * quantised cache: for token i and every KV head, the key and value rows go
+ * to position positions[i] of sequence seq_ids[i].
+ *   k_new, v_new  type (LOCKS_TYPE_*), element (i, h, d) at
+ *                 i * token_stride + h * head_stride + d (strides in
+ *                 elements, d contiguous), so slices of a fused projection
+ *                 need no copy.  Pointers, and strides in bytes, are
+ *                 multiples of 16 (LOCKS_ERR_INVALID_ARG otherwise).
+ *   seq_ids, positions  int32 [n_tokens]; tokens with seq_id < 0 are
+ *                 skipped (padding).  A position may be listed once only:
+ *                 rows of a position listed twice race.
+ *   records       [num_phys_pages][h_kv] records
+ *   page_table    int32 [batch][max_pages]
+ *   status        optional int32 device status word: LOCKS_DEV_BAD_PAIR for
+ *                 a seq_id >= batch or a position outside the table,
+ *                 LOCKS_DEV_BAD_PAGE_ID for a table entry outside the cache
+ *                 (the token is skipped)
+ * LOCKS_ERR_UNSUPPORTED when n_tokens * h_kv exceeds 2^31 - 1. */
+locks_status_t locks_quantise_kv(
+    const void *k_new, const void *v_new, int type, int64_t k_token_stride,
+    int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+    const int32_t *seq_ids, const int32_t *positions, int n_tokens,
+    void *records, int64_t num_phys_pages, int h_kv,
+    const int32_t *page_table, int batch, int max_pages, int32_t *status,
+    locks_stream_t stream);
+
+/* Read pages of the quantised cache back as numbers: for each listed
+ * (seq_ids[i], page_ids[i]) pair and every KV head,
+ *   k_out, v_out  type [n_pairs][h_kv][16][128], 16-byte aligned (either may
+ *                 be NULL): the layout of a bf16 cache of n_pairs pages, so
+ *                 k_out can be given to locks_build_summaries with a page
+ *                 table that numbers its pages.  fp16 rounds, and overflows
+ *                 to infinity above 65504.
+ *   seq_lens      optional int32 [batch]: slots at or past a sequence's
+ *                 length read as zeros (without it every slot is converted,
+ *                 also ones never written)
+ *   status        optional int32 device status word: LOCKS_DEV_BAD_PAIR,
+ *                 LOCKS_DEV_BAD_PAGE_ID (the pair's output is zeros),
+ *                 LOCKS_DEV_BAD_SEQ_LEN
+ * LOCKS_ERR_UNSUPPORTED when n_pairs * h_kv exceeds 2^31 - 1. */
+locks_status_t locks_dequantise_kv(
+    const void *records, int64_t num_phys_pages, int h_kv,
+    const int32_t *page_table, int batch, int max_pages,
+    const int32_t *seq_ids, const int32_t *page_ids, int n_pairs,
+    const int32_t *seq_lens, int type, void *k_out, void *v_out,
+    int32_t *status, locks_stream_t stream);
+
+/* locks_sparse_decode over the quantised cache: the same attention, lists
+ * (idx NULL: every page), outputs, workspace and status bits, with K and V
+ * the numbers that the records stand for.  q and o_out must be 16-byte
+ * aligned.  The query takes part in fp16 after a power-of-two scale per
+ * head, the weights in fp16, sums and softmax statistics in fp32.
+ * LOCKS_ERR_UNSUPPORTED for a batch above 41088. */
+locks_status_t locks_quantised_decode(
+    const void *q, const void *records, int64_t num_phys_pages,
+    const int32_t *page_table, const int32_t *seq_lens, const int32_t *idx,
+    int k, int batch, int h_q, int h_kv, int max_pages, void *o_out,
+    float *lse_out, void *workspace, size_t workspace_bytes,
+    locks_stream_t stream);
+
+/* Attention of one new token per sequence over the quantised cache, every
+ * page of every sequence, where all sequences begin with the same
+ * prefix_pages full pages (a system prompt, a document):
+ *   prefix_table  int32 [prefix_pages]: the shared pages' physical ids.  The
+ *                 first prefix_pages entries of a row of page_table are not
+ *                 read.
+ *   seq_lens      int32 [batch], tokens including the prefix.  A sequence
+ *                 shorter than the prefix attends to its first seq_lens[b]
+ *                 tokens of it.
+ *   prefix_pages  0 .. max_pages (0: locks_quantised_decode without a list)
+ *   workspace     >= locks_prefix_workspace_size bytes, its first int32 the
+ *                 device status word, as for the other calls
+ * Other arguments, numerics and errors as locks_quantised_decode. */
+locks_status_t locks_prefix_decode(
+    const void *q, const void *records, int64_t num_phys_pages,
+    const int32_t *prefix_table, int prefix_pages, const int32_t *page_table,
+    const int32_t *seq_lens, int batch, int h_q, int h_kv, int max_pages,
+    void *o_out, float *lse_out, void *workspace, size_t workspace_bytes,
+    locks_stream_t stream);
+
+/* Workspace bytes of locks_prefix_decode for these sizes. */
+locks_status_t locks_prefix_workspace_size(int batch, int h_q, int h_kv,
+                                           int max_pages, int prefix_pages,
+                                           size_t *bytes);
 
 /* Zero the device status word (the first int32 of `status_word`). */
 locks_status_t locks_clear_status(void *status_word, locks_stream_t stream);

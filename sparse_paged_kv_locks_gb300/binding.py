@@ -19,6 +19,7 @@ PAGE = 16
 HEAD_DIM = 128
 RANK = 8
 RECORD_BYTES = 832
+KV_RECORD_BYTES = 4128        # quantised cache: one (page, KV head)
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib",
                         "liblocks.so")
@@ -83,6 +84,16 @@ _SIGS = {
                                      ctypes.POINTER(ctypes.c_int32), _P]),
     "locks_decoder_last_cuda_error": (_I, [_P]),
     "locks_decoder_destroy": (None, [_P]),
+    "locks_quantise_kv": (_I, [_P, _P, _I, _I64, _I64, _I64, _I64, _P, _P, _I,
+                               _P, _I64, _I, _P, _I, _I, _P, _P]),
+    "locks_dequantise_kv": (_I, [_P, _I64, _I, _P, _I, _I, _P, _P, _I, _P, _I,
+                                 _P, _P, _P, _P]),
+    "locks_quantised_decode": (_I, [_P, _P, _I64, _P, _P, _P, _I, _I, _I, _I,
+                                    _I, _P, _P, _P, _SZ, _P]),
+    "locks_prefix_decode": (_I, [_P, _P, _I64, _P, _I, _P, _P, _I, _I, _I, _I,
+                                 _P, _P, _P, _SZ, _P]),
+    "locks_prefix_workspace_size": (_I, [_I, _I, _I, _I, _I,
+                                         ctypes.POINTER(_SZ)]),
     "locks_clear_status": (_I, [_P, _P]),
     "locks_read_status": (_I, [_P, ctypes.POINTER(ctypes.c_int32), _P]),
 }
@@ -421,6 +432,195 @@ def locks_append_kv(k_new, v_new, k_cache, v_cache, page_table, seq_lens,
         _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache), P, h_kv,
         _ptr(page_table), batch, max_pages, _ptr(seq_lens), _ptr(summaries),
         _ptr(tau_out), flags, _ptr(status), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# the quantised KV cache
+# ---------------------------------------------------------------------------
+_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def new_quantised_cache(num_phys_pages, h_kv, device="cuda"):
+    """Zeroed record cache [num_phys_pages][h_kv][4128] uint8 (keys, values
+    and scales of a page and head in one record, see locks.h)."""
+    return torch.zeros(num_phys_pages, h_kv, KV_RECORD_BYTES,
+                       dtype=torch.uint8, device=device)
+
+
+def locks_prefix_workspace_size(batch, h_q, h_kv, max_pages,
+                                prefix_pages) -> int:
+    out = _SZ(0)
+    _check("locks_prefix_workspace_size",
+           lib().locks_prefix_workspace_size(batch, h_q, h_kv, max_pages,
+                                             prefix_pages,
+                                             ctypes.byref(out)))
+    return int(out.value)
+
+
+def new_prefix_workspace(batch, h_q, h_kv, max_pages, prefix_pages,
+                         device="cuda"):
+    n = locks_prefix_workspace_size(batch, h_q, h_kv, max_pages, prefix_pages)
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _req_rows(t, name):
+    """[n][h_kv][128] rows of any token and head stride, dims contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _TYPES:
+        raise TypeError(f"{name} must be bfloat16, float16 or float32, got "
+                        f"{t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3 or t.shape[2] != HEAD_DIM or t.stride(2) != 1:
+        raise ValueError(f"{name} must be [n][h_kv][128] with contiguous "
+                         "rows")
+    step = 16 // t.element_size()
+    if t.data_ptr() % 16 or any(t.shape[i] > 1 and t.stride(i) % step
+                                for i in (0, 1)):
+        raise ValueError(f"{name}'s rows must start at multiples of 16 bytes")
+
+
+def _req_records(cache):
+    _req(cache, "cache", torch.uint8, 3)
+    if cache.shape[2] != KV_RECORD_BYTES:
+        raise ValueError("cache must be [num_phys_pages][h_kv][4128]")
+    return cache.shape[:2]
+
+
+def _req_pairs(a, b, names):
+    for t, name in zip((a, b), names):
+        _req(t, name, torch.int32, 1)
+    if a.numel() != b.numel():
+        raise ValueError(f"{names[0]} and {names[1]} differ in length")
+
+
+def _req_same_device(cache, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != cache.device:
+            raise ValueError(f"{name} and cache are on different devices")
+
+
+def locks_quantise_kv(k_new, v_new, seq_ids, positions, page_table, cache,
+                      status=None, stream=None):
+    """Rows k_new, v_new [n][h_kv][128] (bfloat16, float16 or float32; token
+    and head strides free) into position positions[i] of sequence
+    seq_ids[i] (seq_id < 0: skipped)."""
+    P, h_kv = _req_records(cache)
+    _req_rows(k_new, "k_new")
+    _req_rows(v_new, "v_new")
+    _req_pairs(seq_ids, positions, ("seq_ids", "positions"))
+    _req(page_table, "page_table", torch.int32, 2)
+    n = seq_ids.numel()
+    if tuple(k_new.shape) != (n, h_kv, HEAD_DIM) or \
+            k_new.shape != v_new.shape or k_new.dtype != v_new.dtype:
+        raise ValueError("k_new and v_new must be [n][h_kv][128] of one type")
+    if status is not None:
+        _req(status, "status", torch.int32)
+    _req_same_device(cache, k_new=k_new, v_new=v_new, seq_ids=seq_ids,
+                     positions=positions, page_table=page_table,
+                     status=status)
+    batch, max_pages = page_table.shape
+    # the stride of a dimension of one entry says nothing
+    ks, vs = ([t.stride(i) if t.shape[i] > 1 else 0 for i in (0, 1)]
+              for t in (k_new, v_new))
+    _check("locks_quantise_kv", lib().locks_quantise_kv(
+        _ptr(k_new), _ptr(v_new), _TYPES[k_new.dtype], *ks, *vs,
+        _ptr(seq_ids), _ptr(positions), n, _ptr(cache), P, h_kv,
+        _ptr(page_table), batch, max_pages, _ptr(status), _stream(stream)))
+
+
+def locks_dequantise_kv(cache, page_table, seq_ids, page_ids, k_out, v_out,
+                        seq_lens=None, status=None, stream=None):
+    """Pages (seq_ids[i], page_ids[i]) back as numbers in k_out, v_out
+    [n][h_kv][16][128] (bfloat16, float16 or float32; either may be None);
+    with seq_lens, slots past a sequence's end read as zeros."""
+    P, h_kv = _req_records(cache)
+    _req_pairs(seq_ids, page_ids, ("seq_ids", "page_ids"))
+    _req(page_table, "page_table", torch.int32, 2)
+    n = seq_ids.numel()
+    outs = [t for t in (k_out, v_out) if t is not None]
+    if not outs:
+        raise ValueError("k_out or v_out must be given")
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or t.dtype not in _TYPES:
+            raise TypeError(f"{name} must be a bfloat16, float16 or float32 "
+                            "tensor")
+        _req(t, name, outs[0].dtype, 4)
+        if tuple(t.shape) != (n, h_kv, PAGE, HEAD_DIM):
+            raise ValueError(f"{name} must be [n][h_kv][16][128]")
+    batch, max_pages = page_table.shape
+    if seq_lens is not None:
+        _req(seq_lens, "seq_lens", torch.int32, 1)
+        if seq_lens.numel() != batch:
+            raise ValueError("seq_lens must have one entry per sequence")
+    if status is not None:
+        _req(status, "status", torch.int32)
+    _req_same_device(cache, page_table=page_table, seq_ids=seq_ids,
+                     page_ids=page_ids, k_out=k_out, v_out=v_out,
+                     seq_lens=seq_lens, status=status)
+    _check("locks_dequantise_kv", lib().locks_dequantise_kv(
+        _ptr(cache), P, h_kv, _ptr(page_table), batch, max_pages,
+        _ptr(seq_ids), _ptr(page_ids), n, _ptr(seq_lens),
+        _TYPES[outs[0].dtype], _ptr(k_out), _ptr(v_out), _ptr(status),
+        _stream(stream)))
+
+
+def _req_decode(q, cache, page_table, seq_lens, o_out, lse_out, workspace,
+                **more):
+    P, h_kv = _req_records(cache)
+    _req(q, "q", torch.bfloat16, 3)
+    _req(page_table, "page_table", torch.int32, 2)
+    _req(seq_lens, "seq_lens", torch.int32, 1)
+    _req(o_out, "o_out", torch.bfloat16, 3)
+    _req(lse_out, "lse_out", torch.float32, 2)
+    _req(workspace, "workspace", torch.uint8, 1)
+    batch, h_q, d = q.shape
+    if d != HEAD_DIM or o_out.shape != q.shape or \
+            tuple(lse_out.shape) != (batch, h_q):
+        raise ValueError("q and o_out must be [batch][h_q][128], lse_out "
+                         "[batch][h_q]")
+    if page_table.shape[0] != batch or seq_lens.numel() != batch:
+        raise ValueError("page_table and seq_lens must have one entry per "
+                         "sequence")
+    _req_same_device(cache, q=q, page_table=page_table, seq_lens=seq_lens,
+                     o_out=o_out, lse_out=lse_out, workspace=workspace,
+                     **more)
+    return P, h_kv, batch, h_q, page_table.shape[1]
+
+
+def locks_quantised_decode(q, cache, page_table, seq_lens, idx, k, o_out,
+                           lse_out, workspace, stream=None):
+    """locks_sparse_decode over the quantised cache (idx None: every
+    page)."""
+    P, h_kv, batch, h_q, max_pages = _req_decode(
+        q, cache, page_table, seq_lens, o_out, lse_out, workspace, idx=idx)
+    if idx is not None:
+        _req(idx, "idx", torch.int32, 3)
+        if tuple(idx.shape) != (batch, h_kv, k):
+            raise ValueError("idx must be [batch][h_kv][k]")
+    _check("locks_quantised_decode", lib().locks_quantised_decode(
+        _ptr(q), _ptr(cache), P, _ptr(page_table), _ptr(seq_lens), _ptr(idx),
+        k, batch, h_q, h_kv, max_pages, _ptr(o_out), _ptr(lse_out),
+        _ptr(workspace), workspace.numel(), _stream(stream)))
+
+
+def locks_prefix_decode(q, cache, prefix_table, page_table, seq_lens, o_out,
+                        lse_out, workspace, stream=None):
+    """Attention over every page, where all sequences begin with the pages
+    prefix_table [prefix_pages] (their tables' first entries are not
+    read)."""
+    _req(prefix_table, "prefix_table", torch.int32, 1)
+    P, h_kv, batch, h_q, max_pages = _req_decode(
+        q, cache, page_table, seq_lens, o_out, lse_out, workspace,
+        prefix_table=prefix_table)
+    _check("locks_prefix_decode", lib().locks_prefix_decode(
+        _ptr(q), _ptr(cache), P, _ptr(prefix_table), prefix_table.numel(),
+        _ptr(page_table), _ptr(seq_lens), batch, h_q, h_kv, max_pages,
+        _ptr(o_out), _ptr(lse_out), _ptr(workspace), workspace.numel(),
+        _stream(stream)))
 
 
 def locks_clear_status(status_word, stream=None):

@@ -55,6 +55,24 @@ static size_t decode_region(int batch, int h_q, int h_kv, int list_len) {
          round_up(rows * 4, 256);
 }
 
+// the same region as the quantised cache's decode lays it out
+struct DecodeRegion {
+  int *meta;
+  float *o_part;
+  float2 *ml_part;
+  size_t bytes;
+};
+// partials hold 128 sums, a reference and a sum of weights per head
+static DecodeRegion qdecode_region(uint8_t *at, int batch, int h_q, int h_kv,
+                                   int list_len) {
+  const size_t rows = decode_slots(batch, h_kv, list_len) * (size_t)(h_q / h_kv);
+  const size_t meta = decode_meta_bytes(batch);
+  const size_t sums = round_up(rows * kDim * 4, 256);
+  return {reinterpret_cast<int *>(at), reinterpret_cast<float *>(at + meta),
+          reinterpret_cast<float2 *>(at + meta + sums),
+          meta + sums + round_up(rows * 8, 256)};
+}
+
 static bool heads_ok(int h_q, int h_kv) {
   return h_kv >= 1 && h_q >= h_kv && h_q % h_kv == 0;
 }
@@ -178,7 +196,10 @@ locks_status_t locks_workspace_size(int batch, int h_q, int h_kv,
   if (h_q / h_kv > kMaxGroup) return LOCKS_ERR_UNSUPPORTED;
   const size_t a = score_region(batch, h_q, h_kv, max_pages);
   const size_t b = decode_region(batch, h_q, h_kv, k);
-  *bytes = kWsHeader + (a > b ? a : b);
+  const size_t c = qdecode_region(nullptr, batch, h_q, h_kv, k).bytes;
+  size_t most = a > b ? a : b;
+  if (c > most) most = c;
+  *bytes = kWsHeader + most;
   return LOCKS_OK;
 }
 
@@ -418,6 +439,161 @@ locks_status_t locks_append_kv_ex(const void *k_new, const void *v_new,
                                 h_kv, page_table, batch, max_pages, seq_lens,
                                 summaries, tau_out, flags, status,
                                 (cudaStream_t)stream);
+  return e == cudaSuccess ? LOCKS_OK : fail_cuda(e);
+}
+
+// ---------------------------------------------------------------------------
+// quantised KV cache
+// ---------------------------------------------------------------------------
+static bool aligned16(const void *p) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
+}
+
+static bool type_ok(int type) {
+  return type == LOCKS_TYPE_BF16 || type == LOCKS_TYPE_FP16 ||
+         type == LOCKS_TYPE_FP32;
+}
+
+locks_status_t locks_quantise_kv(
+    const void *k_new, const void *v_new, int type, int64_t k_token_stride,
+    int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+    const int32_t *seq_ids, const int32_t *positions, int n_tokens,
+    void *records, int64_t num_phys_pages, int h_kv,
+    const int32_t *page_table, int batch, int max_pages, int32_t *status,
+    locks_stream_t stream) {
+  if (!type_ok(type) || n_tokens < 0 || h_kv < 1 || batch < 1 ||
+      max_pages < 1 || num_phys_pages < 1)
+    return LOCKS_ERR_INVALID_ARG;
+  if ((long long)n_tokens * h_kv > 0x7fffffffLL ||
+      (long long)max_pages * kPage > 0x7fffffffLL)
+    return LOCKS_ERR_UNSUPPORTED;
+  if (n_tokens == 0) return LOCKS_OK;
+  if (!k_new || !v_new || !seq_ids || !positions || !records || !page_table)
+    return LOCKS_ERR_INVALID_ARG;
+  // 16 bytes of elements
+  const int64_t step = type == LOCKS_TYPE_FP32 ? 4 : 8;
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(records) ||
+      k_token_stride % step || k_head_stride % step || v_token_stride % step ||
+      v_head_stride % step)
+    return LOCKS_ERR_INVALID_ARG;
+  cudaError_t e = launch_quantise(
+      k_new, v_new, type, k_token_stride, k_head_stride, v_token_stride,
+      v_head_stride, seq_ids, positions, n_tokens, records, num_phys_pages,
+      h_kv, page_table, batch, max_pages, status, (cudaStream_t)stream);
+  return e == cudaSuccess ? LOCKS_OK : fail_cuda(e);
+}
+
+locks_status_t locks_dequantise_kv(
+    const void *records, int64_t num_phys_pages, int h_kv,
+    const int32_t *page_table, int batch, int max_pages,
+    const int32_t *seq_ids, const int32_t *page_ids, int n_pairs,
+    const int32_t *seq_lens, int type, void *k_out, void *v_out,
+    int32_t *status, locks_stream_t stream) {
+  if (!type_ok(type) || n_pairs < 0 || h_kv < 1 || batch < 1 ||
+      max_pages < 1 || num_phys_pages < 1)
+    return LOCKS_ERR_INVALID_ARG;
+  if ((long long)n_pairs * h_kv > 0x7fffffffLL ||
+      (long long)max_pages * kPage > 0x7fffffffLL)
+    return LOCKS_ERR_UNSUPPORTED;
+  if (n_pairs == 0) return LOCKS_OK;
+  if (!records || !page_table || !seq_ids || !page_ids || (!k_out && !v_out))
+    return LOCKS_ERR_INVALID_ARG;
+  if (!aligned16(records) || !aligned16(k_out) || !aligned16(v_out))
+    return LOCKS_ERR_INVALID_ARG;
+  cudaError_t e = launch_dequantise(
+      records, num_phys_pages, h_kv, page_table, batch, max_pages, seq_ids,
+      page_ids, n_pairs, seq_lens, type, k_out, v_out, status,
+      (cudaStream_t)stream);
+  return e == cudaSuccess ? LOCKS_OK : fail_cuda(e);
+}
+
+// checks shared by the two attention calls (pointers after the empty batch)
+static locks_status_t check_qdecode(const void *q, const void *records,
+                                    int64_t num_phys_pages,
+                                    const int32_t *page_table,
+                                    const int32_t *seq_lens, int list_len,
+                                    int batch, int h_q, int h_kv,
+                                    int max_pages, const void *o_out,
+                                    const float *lse_out,
+                                    const void *workspace) {
+  if (batch < 0 || max_pages < 1 || num_phys_pages < 1 || !heads_ok(h_q, h_kv))
+    return LOCKS_ERR_INVALID_ARG;
+  if (list_len < 1) return LOCKS_ERR_INVALID_ARG;
+  if (h_q / h_kv > kMaxGroup) return LOCKS_ERR_UNSUPPORTED;
+  if (batch > qdecode_max_batch() || h_kv > 65535) return LOCKS_ERR_UNSUPPORTED;
+  if ((long long)max_pages * kPage > 0x7fffffffLL ||
+      (long long)batch * h_kv * list_len > 0x7fffffffLL)
+    return LOCKS_ERR_UNSUPPORTED;
+  if (batch == 0) return LOCKS_OK;
+  if (!q || !records || !page_table || !seq_lens || !o_out || !lse_out ||
+      !workspace)
+    return LOCKS_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(records) || !aligned16(o_out) ||
+      !aligned16(workspace))
+    return LOCKS_ERR_INVALID_ARG;
+  return LOCKS_OK;
+}
+
+locks_status_t locks_quantised_decode(
+    const void *q, const void *records, int64_t num_phys_pages,
+    const int32_t *page_table, const int32_t *seq_lens, const int32_t *idx,
+    int k, int batch, int h_q, int h_kv, int max_pages, void *o_out,
+    float *lse_out, void *workspace, size_t workspace_bytes,
+    locks_stream_t stream) {
+  const int list_len = idx ? k : max_pages;
+  locks_status_t st =
+      check_qdecode(q, records, num_phys_pages, page_table, seq_lens, list_len,
+                    batch, h_q, h_kv, max_pages, o_out, lse_out, workspace);
+  if (st != LOCKS_OK || batch == 0) return st;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  const DecodeRegion r =
+      qdecode_region(ws + kWsHeader, batch, h_q, h_kv, list_len);
+  if (workspace_bytes < kWsHeader + r.bytes) return LOCKS_ERR_WORKSPACE;
+  cudaError_t e = launch_qdecode(
+      q, records, num_phys_pages, page_table, seq_lens, idx, k, batch, h_kv,
+      h_q / h_kv, max_pages, nullptr, 0,
+      (int)decode_warps_cap(batch, h_kv, list_len), o_out, lse_out, r.o_part,
+      r.ml_part, r.meta, nullptr, nullptr, 0, reinterpret_cast<int32_t *>(ws),
+      (cudaStream_t)stream);
+  return e == cudaSuccess ? LOCKS_OK : fail_cuda(e);
+}
+
+locks_status_t locks_prefix_workspace_size(int batch, int h_q, int h_kv,
+                                           int max_pages, int prefix_pages,
+                                           size_t *bytes) {
+  if (!bytes || batch < 0 || max_pages < 1 || prefix_pages < 0 ||
+      prefix_pages > max_pages || !heads_ok(h_q, h_kv))
+    return LOCKS_ERR_INVALID_ARG;
+  if (h_q / h_kv > kMaxGroup) return LOCKS_ERR_UNSUPPORTED;
+  *bytes =
+      kWsHeader + qdecode_region(nullptr, batch, h_q, h_kv, max_pages).bytes;
+  return LOCKS_OK;
+}
+
+locks_status_t locks_prefix_decode(
+    const void *q, const void *records, int64_t num_phys_pages,
+    const int32_t *prefix_table, int prefix_pages, const int32_t *page_table,
+    const int32_t *seq_lens, int batch, int h_q, int h_kv, int max_pages,
+    void *o_out, float *lse_out, void *workspace, size_t workspace_bytes,
+    locks_stream_t stream) {
+  if (prefix_pages < 0 || prefix_pages > max_pages)
+    return LOCKS_ERR_INVALID_ARG;
+  locks_status_t st =
+      check_qdecode(q, records, num_phys_pages, page_table, seq_lens,
+                    max_pages, batch, h_q, h_kv, max_pages, o_out, lse_out,
+                    workspace);
+  if (st != LOCKS_OK || batch == 0) return st;
+  if (prefix_pages > 0 && !prefix_table) return LOCKS_ERR_INVALID_ARG;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  const DecodeRegion r =
+      qdecode_region(ws + kWsHeader, batch, h_q, h_kv, max_pages);
+  if (workspace_bytes < kWsHeader + r.bytes) return LOCKS_ERR_WORKSPACE;
+  cudaError_t e = launch_qdecode(
+      q, records, num_phys_pages, page_table, seq_lens, nullptr, 0, batch,
+      h_kv, h_q / h_kv, max_pages, prefix_table, prefix_pages,
+      (int)decode_warps_cap(batch, h_kv, max_pages), o_out, lse_out, r.o_part,
+      r.ml_part, r.meta, nullptr, nullptr, 0, reinterpret_cast<int32_t *>(ws),
+      (cudaStream_t)stream);
   return e == cudaSuccess ? LOCKS_OK : fail_cuda(e);
 }
 

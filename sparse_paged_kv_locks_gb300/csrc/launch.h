@@ -161,6 +161,36 @@ cudaError_t launch_variant_bits(int rank, const void *q, const void *records,
                                 int G, int max_pages, float *scores,
                                 int32_t *status, cudaStream_t stream);
 
+// the quantised KV cache (quantise.cu, qdecode.cu)
+cudaError_t launch_quantise(const void *k_new, const void *v_new, int type,
+                            int64_t k_token, int64_t k_head, int64_t v_token,
+                            int64_t v_head, const int32_t *seq_ids,
+                            const int32_t *positions, int n_tokens,
+                            void *records, int64_t num_phys, int h_kv,
+                            const int32_t *pt, int batch, int max_pages,
+                            int32_t *status, cudaStream_t stream);
+
+cudaError_t launch_dequantise(const void *records, int64_t num_phys, int h_kv,
+                              const int32_t *pt, int batch, int max_pages,
+                              const int32_t *seq_ids, const int32_t *page_ids,
+                              int n_pairs, const int32_t *seq_lens, int type,
+                              void *k_out, void *v_out, int32_t *status,
+                              cudaStream_t stream);
+
+// prefix, prefix_pages: pages that every sequence begins with (null, 0:
+// none).  o_part, ml_part, meta: the split form's partials (sums not
+// divided; reference and sum of weights) and position layout.
+cudaError_t launch_qdecode(const void *q, const void *records,
+                           int64_t num_phys, const int32_t *pt,
+                           const int32_t *seq_lens, const int32_t *idx, int k,
+                           int batch, int h_kv, int G, int max_pages,
+                           const int32_t *prefix, int prefix_pages,
+                           int max_warps, void *o_out, float *lse_out,
+                           float *o_part, float2 *ml_part, int *meta,
+                           const float *shared_o, const float2 *shared_ml,
+                           int shared, int32_t *status, cudaStream_t stream);
+int qdecode_max_batch();
+
 size_t variant_record_bytes(int rank, int vbits);
 // largest batch whose per-sequence tables fit beside the variant's ring
 int variant_max_batch(int rank, int vbits);

@@ -1,0 +1,752 @@
+// Attention of one new token per sequence over the quantised KV cache: for
+// every query head, x_t = q . k_t / sqrt(128), o = sum softmax(x)_t v_t and
+// lse = ln sum exp(x_t), over the tokens of the listed pages (or of all).
+//
+// With keys k = 2^ek * c, values v = 2^ev * d (codes c, d) and f = log2(e) /
+// sqrt(128),
+//   w_t = 2^(f 2^ek_t (q . c_t) + ev_t - m + 8)
+//   o   = sum w_t d_t / sum w_t 2^-ev_t
+//   lse = ln 2 * (log2(sum w_t 2^-ev_t) + m - 8)
+// so a value's scale is part of its weight and one running reference m (of
+// score plus value exponent) serves both sums.  m is raised, and the sums
+// rescaled, only when a term passes it by more than 2^7: weights stay below
+// 2^15 and, in fp16, keep full precision down to 2^-22 of the largest
+// contribution and some down to 2^-32.  Codes are exact in fp16, and so is
+// the query after a power-of-two scale per head (elements 2^-22 below its
+// largest lose bits); products, sums and references are fp32.
+//
+// Bound: memory, 4128 bytes per listed page and KV head.  One bulk copy
+// brings a record into a warp's private ring in shared memory, so the warps
+// run free of one another.  Tokens (then dims) are the M dimension of
+// mma.m16n8k16 and the query heads the N dimension: a group of up to 8 heads
+// is one column tile, and the page's 16 tokens fill M.  The order of dims in
+// the products is free, so a lane's A fragments are whole 16-byte groups of a
+// key row, and for the second product the 16 dims of one group.
+#include "launch.h"
+#include "quantised.cuh"
+
+namespace locks {
+
+constexpr int kQdWarps = 4;
+constexpr int kQdThreads = 32 * kQdWarps;
+constexpr int kQdStages = 4;
+constexpr int kQdStride = 4224;  // ring stage: a record, 128-byte aligned
+constexpr int kQdWarpRing = kQdStages * kQdStride;
+constexpr int kQdRing = kQdWarps * kQdWarpRing;
+constexpr float kQdScale = 0.12751743074602467f;  // log2(e) / sqrt(128)
+constexpr float kQdLn2 = 0.69314718055994531f;
+constexpr float kQdLift = 8.f;    // weights are 2^(.. - m + 8)
+constexpr float kQdSlack = 7.f;   // .. and m trails the maximum by at most 7
+
+// One lane's entry of a window of 32 positions.
+struct QEntry {
+  int phys, ntok, u;  // phys < 0: nothing to read
+};
+
+struct QdArgs {
+  const __nv_bfloat16 *q;
+  const uint8_t *records;
+  int64_t num_phys;
+  const int32_t *pt, *seq_lens, *idx;
+  int k, batch, h_kv, G, max_pages, n_warps;
+  // pages that every sequence begins with (null, 0: none)
+  const int32_t *prefix;
+  int prefix_pages;
+  __nv_bfloat16 *o_out;
+  float *lse_out;
+  float *o_part;     // [slot][G][128], sums not divided
+  float2 *ml_part;   // [slot][G] (m, sum of weights)
+  int *meta;         // run length, then the sequences' first positions
+  int32_t *status;
+};
+
+// pages of sequence b's own list, for lists that are not given
+__device__ __forceinline__ int own_pages(const QdArgs &a, int L) {
+  return (L + kPage - 1) / kPage;
+}
+
+__device__ __forceinline__ QEntry q_resolve(const QdArgs &a,
+                                            const PageLists &lists, int p,
+                                            int pe) {
+  QEntry e{-1, 0, 0};
+  if (p >= pe) return e;
+  const int b = lists.sequence(p);
+  const int len = lists.length(b);
+  const int r = p - lists.first(b);
+  const int h = r / len;
+  int pg = r - h * len;
+  e.u = b * lists.h_kv + h;
+  const int L = checked_len(a.seq_lens, b, a.max_pages, a.status);
+  const int n = (L + kPage - 1) / kPage;
+  const int32_t *table = a.pt + (size_t)b * a.max_pages;
+  if (a.idx) {
+    pg = __ldg(a.idx + (size_t)e.u * a.k + pg);
+    if (pg < 0) return e;
+    if (pg >= n) {
+      set_status(a.status, LOCKS_DEV_BAD_INDEX);
+      return e;
+    }
+  } else if (pg < a.prefix_pages) {
+    table = a.prefix;
+  }
+  const int ph = __ldg(table + pg);
+  if (ph < 0 || ph >= a.num_phys) {
+    set_status(a.status, LOCKS_DEV_BAD_PAGE_ID);
+    return e;
+  }
+  e.phys = ph;
+  e.ntok = min(kPage, L - pg * kPage);
+  return e;
+}
+
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  return h2_as_u32(__floats2half2_rn(lo, hi));
+}
+__device__ __forceinline__ uint32_t byte_perm(uint32_t a, uint32_t b,
+                                              uint32_t sel) {
+  return __byte_perm(a, b, sel);
+}
+__device__ __forceinline__ uint32_t pack_bf2q(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// NT: column tiles of 8 query heads (1: G <= 8, 2: G <= 16).
+// UNIT: lists of k entries each, one unit to a CTA or cluster, merged on
+// chip; otherwise every warp takes a run of positions and units that span
+// runs are merged by merge_kernel.
+template <int NT, bool UNIT>
+__global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
+    qdecode_kernel(const QdArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t s_bar[kQdWarps][kQdStages];
+  int *s_pre = reinterpret_cast<int *>(smem + kQdRing);  // [batch + 1]
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int h_q = a.h_kv * a.G;
+  const PageLists lists{s_pre, a.batch, a.h_kv, a.idx ? a.h_kv * a.k : 0};
+  uint64_t *bar = s_bar[wid];
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < kQdStages; ++i) mbar_init(bar + i, 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  pdl_wait();
+  pdl_trigger();
+
+  int total;
+  if (a.idx) {
+    total = a.batch * a.h_kv * a.k;
+  } else {
+    for (int b = threadIdx.x; b < a.batch; b += kQdThreads)
+      s_pre[b + 1] =
+          a.h_kv * own_pages(a, checked_len(a.seq_lens, b, a.max_pages,
+                                            blockIdx.x ? nullptr : a.status));
+    if (threadIdx.x == 0) s_pre[0] = 0;
+    __syncthreads();
+    if (wid == 0) {
+      int run = 0;  // of the entries before this block of 32
+      for (int b0 = 1; b0 <= a.batch; b0 += 32) {
+        int v = b0 + lane <= a.batch ? s_pre[b0 + lane] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int w = __shfl_up_sync(0xffffffffu, v, o);
+          if (lane >= o) v += w;
+        }
+        if (b0 + lane <= a.batch) s_pre[b0 + lane] = run + v;
+        run += __shfl_sync(0xffffffffu, v, 31);
+      }
+    }
+    __syncthreads();
+    total = s_pre[a.batch];
+  }
+
+  // this warp's run of positions [pb, pe)
+  const int gw = blockIdx.x * kQdWarps + wid;
+  const int ucl = UNIT ? (int)cluster_nctarank() : 1;
+  const int urank = UNIT && ucl > 1 ? (int)cluster_ctarank() : 0;
+  const int unit0 = UNIT ? (int)blockIdx.x / ucl : 0;
+  int pb, pe, chunk = 0;
+  if constexpr (UNIT) {
+    const int sl = urank * kQdWarps + wid, nsl = ucl * kQdWarps;
+    pb = unit0 * a.k + (int)((long long)sl * a.k / nsl);
+    pe = unit0 * a.k + (int)((long long)(sl + 1) * a.k / nsl);
+  } else {
+    chunk = (int)max(1LL, ((long long)total + a.n_warps - 1) / a.n_warps);
+    if (blockIdx.x == 0) {  // for the merge
+      if (threadIdx.x == 0) a.meta[0] = chunk;
+      if (!a.idx)
+        for (int b = threadIdx.x; b <= a.batch; b += kQdThreads)
+          a.meta[1 + b] = s_pre[b];
+    }
+    const long long from = (long long)gw * chunk;
+    if (gw >= a.n_warps || from >= total) return;
+    pb = (int)from;
+    pe = min(total, pb + chunk);
+  }
+
+  uint8_t *ring = smem + wid * kQdWarpRing;
+  const uint32_t ring_s = smem_u32(ring);
+
+  // window of 32 positions: this lane's entry, and those not yet copied
+  int win = pb - 32;
+  uint32_t left = 0;
+  QEntry we{-1, 0, 0};
+  auto next = [&](int &phys, int &ntok, int &u) {
+    while (left == 0) {
+      win += 32;
+      if (win >= pe) {
+        phys = -1;
+        return;
+      }
+      we = q_resolve(a, lists, win + lane, pe);
+      left = __ballot_sync(0xffffffffu, we.phys >= 0);
+    }
+    const int j = __ffs(left) - 1;
+    left &= left - 1;
+    phys = __shfl_sync(0xffffffffu, we.phys, j);
+    ntok = __shfl_sync(0xffffffffu, we.ntok, j);
+    u = __shfl_sync(0xffffffffu, we.u, j);
+  };
+  auto issue = [&](int st, int phys, int u) {
+    if (lane == 0) {
+      mbar_arrive_tx(bar + st, kQRec);
+      bulk_g2s(ring + st * kQdStride,
+               a.records + ((size_t)phys * a.h_kv + u % a.h_kv) * kQRec, kQRec,
+               bar + st);
+    }
+  };
+  // copies in flight, oldest first (tokens 0: none)
+  int fn[kQdStages], fu[kQdStages];
+#pragma unroll
+  for (int i = 0; i < kQdStages; ++i) {
+    int phys;
+    fn[i] = fu[i] = 0;
+    next(phys, fn[i], fu[i]);
+    if (phys < 0)
+      fn[i] = 0;
+    else
+      issue(i, phys, fu[i]);
+  }
+
+  // query B fragments of a unit: column n = head 8 nt + g of the group,
+  // k-step 4 j + w of the product over dims 16 (t + 4 j) + 4 w .. + 3; f:
+  // factors of the scores of heads 8 nt + 2t, 2t + 1
+  uint32_t qb[NT][8][2];
+  float f[NT][2];
+  auto load_q = [&](int u) {
+    const int b = u / a.h_kv, h = u - b * a.h_kv;
+    const __nv_bfloat16 *qu = a.q + ((size_t)b * h_q + (size_t)h * a.G) * kDim;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const bool in = 8 * nt + g < a.G;
+      uint32_t raw[16];
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // 16-byte loads: group t + 4 (i / 2)
+        const uint4 v =
+            in ? __ldg(reinterpret_cast<const uint4 *>(
+                     qu + (8 * nt + g) * kDim + 16 * (t + 4 * (i >> 1)) +
+                     8 * (i & 1)))
+               : make_uint4(0u, 0u, 0u, 0u);
+        raw[4 * i] = v.x;
+        raw[4 * i + 1] = v.y;
+        raw[4 * i + 2] = v.z;
+        raw[4 * i + 3] = v.w;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        top = fmaxf(top, fmaxf(fabsf(bf16_lo(raw[i])), fabsf(bf16_hi(raw[i]))));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // largest magnitude to [2^7, 2^8)
+      const int e = max(-100, (int)(__float_as_uint(top) >> 23) - 127) - 7;
+      const float down = exp2_int(-e);
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        qb[nt][i >> 1][i & 1] =
+            pack_h2(bf16_lo(raw[i]) * down, bf16_hi(raw[i]) * down);
+      const float fe = exp2_int(e) * kQdScale;
+      f[nt][0] = __shfl_sync(0xffffffffu, fe, 8 * t);
+      f[nt][1] = __shfl_sync(0xffffffffu, fe, 8 * t + 4);
+    }
+  };
+
+  // sums: tile i holds dims 16 g + 2 i (elements 0, 1) and 16 g + 2 i + 1
+  // (2, 3) of heads 8 nt + 2t (0, 2) and 8 nt + 2t + 1 (1, 3)
+  float o[NT][8][4], m[NT][2], l[NT][2];
+  auto reset = [&]() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
+  };
+  reset();
+
+  // the unit's sums so far: the result where the unit lies in this run
+  // alone, else a partial (slot unit + warp, distinct for distinct pieces
+  // because both grow along the positions; UNIT: this warp's ring)
+  auto flush = [&](int u) {
+    const int b = u / a.h_kv, h = u - b * a.h_kv;
+    bool whole = false;
+    if constexpr (!UNIT) {
+      const int2 sp = lists.span(u);
+      whole = !a.prefix_pages && sp.x >= pb && sp.y <= pe;
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float ls = l[nt][c];
+        ls += __shfl_xor_sync(0xffffffffu, ls, 4);
+        ls += __shfl_xor_sync(0xffffffffu, ls, 8);
+        ls += __shfl_xor_sync(0xffffffffu, ls, 16);
+        const int hd = 8 * nt + 2 * t + c;
+        if (hd >= a.G) continue;
+        if (whole) {
+          const size_t row = (size_t)b * h_q + (size_t)h * a.G + hd;
+          const float inv = ls == 0.f ? 0.f : 1.f / ls;
+          uint4 *dst = reinterpret_cast<uint4 *>(a.o_out + row * kDim + 16 * g);
+          uint32_t w[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            w[i] = pack_bf2q(o[nt][i][c] * inv, o[nt][i][2 + c] * inv);
+          dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          if (g == 0)
+            a.lse_out[row] = ls == 0.f
+                                 ? -INFINITY
+                                 : (log2f(ls) + (m[nt][c] - kQdLift)) * kQdLn2;
+        } else {
+          float *po = UNIT ? reinterpret_cast<float *>(ring) + hd * kDim
+                           : a.o_part + (((size_t)u + gw) * a.G + hd) * kDim;
+          float2 *ml =
+              UNIT ? reinterpret_cast<float2 *>(ring + 8 * NT * kDim * 4) + hd
+                   : a.ml_part + ((size_t)u + gw) * a.G + hd;
+          float4 *dst = reinterpret_cast<float4 *>(po + 16 * g);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            dst[i] = make_float4(o[nt][2 * i][c], o[nt][2 * i][2 + c],
+                                 o[nt][2 * i + 1][c], o[nt][2 * i + 1][2 + c]);
+          if (g == 0) *ml = make_float2(m[nt][c], ls);
+        }
+      }
+  };
+
+  int cur = UNIT ? unit0 : lists.unit(pb);
+  bool q_ready = false, dead = false;
+  auto advance = [&](int u) {  // close the units before u
+    while (cur < u) {
+      const int2 sp = lists.span(cur);
+      if (sp.y > sp.x) {
+        flush(cur);
+        reset();
+      }
+      ++cur;
+      q_ready = false;
+    }
+  };
+
+  uint32_t phase = 0;
+  for (int st = 0; fn[0] > 0;) {
+    const int ntok = fn[0];
+    if (!UNIT && fu[0] != cur) advance(fu[0]);
+    if (!q_ready) {
+      load_q(cur);
+      q_ready = true;
+    }
+    if (!mbar_wait(bar + st, phase)) {
+      dead = true;
+      break;
+    }
+    const uint32_t rec = ring_s + st * kQdStride;
+
+    // key codes of tokens g, g + 8: groups t, t + 4; value codes of tokens
+    // 2t, 2t + 1, 2t + 8, 2t + 9: group g
+    uint4 kc[2][2], vc[4];
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        kc[r][j] = lds128(rec + (g + 8 * r) * kDim +
+                          16 * q_group(t + 4 * j, g));
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int tok = 2 * t + (r & 1) + 8 * (r >> 1);
+      vc[r] = lds128(rec + kQOffV + tok * kDim + 16 * q_group(g, tok));
+    }
+    float ks[2], ev[2], vi[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      uint32_t ek, e2;
+      asm volatile("ld.shared.u8 %0, [%1];\n"
+                   : "=r"(ek)
+                   : "r"(rec + kQOffKE + g + 8 * r));
+      asm volatile("ld.shared.u8 %0, [%1];\n"
+                   : "=r"(e2)
+                   : "r"(rec + kQOffVE + g + 8 * r));
+      ks[r] = __uint_as_float(ek << 23);
+      ev[r] = (float)((int)e2 - 127);
+      vi[r] = __uint_as_float((254u - e2) << 23);
+    }
+    if (ntok < kPage) {  // rows past the end hold anything
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (2 * t + (r & 1) + 8 * (r >> 1) >= ntok)
+          vc[r] = make_uint4(0u, 0u, 0u, 0u);
+    }
+
+    // scores: rows = tokens, columns = heads
+    float s[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+      s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t k0[4] = {kc[0][j].x, kc[0][j].y, kc[0][j].z, kc[0][j].w};
+      const uint32_t k1[4] = {kc[1][j].x, kc[1][j].y, kc[1][j].z, kc[1][j].w};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t fa[4] = {e4m3x2_lo(k0[w]), e4m3x2_lo(k1[w]),
+                                e4m3x2_hi(k0[w]), e4m3x2_hi(k1[w])};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma_f16(s[nt], fa, qb[nt][4 * j + w][0], qb[nt][4 * j + w][1]);
+      }
+    }
+
+    // weights
+    const bool in0 = g < ntok, in1 = g + 8 < ntok;
+    float z[NT][4];
+    bool raise = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        z[nt][c] = in0 ? fmaf(s[nt][c], f[nt][c] * ks[0], ev[0]) : -INFINITY;
+        z[nt][2 + c] =
+            in1 ? fmaf(s[nt][2 + c], f[nt][c] * ks[1], ev[1]) : -INFINITY;
+        raise |= fmaxf(z[nt][c], z[nt][2 + c]) > m[nt][c] + kQdSlack;
+      }
+    if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float top = fmaxf(z[nt][c], z[nt][2 + c]);
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+          top = fmaxf(top, m[nt][c]);
+          const float fall = m[nt][c] == top ? 1.f : ex2_fast(m[nt][c] - top);
+          m[nt][c] = top;
+          l[nt][c] *= fall;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            o[nt][i][c] *= fall;
+            o[nt][i][2 + c] *= fall;
+          }
+        }
+    }
+    uint32_t pb0[NT], pb1[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float w[4];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float ref = m[nt][c] - kQdLift;
+        w[c] = in0 ? ex2_fast(z[nt][c] - ref) : 0.f;
+        w[2 + c] = in1 ? ex2_fast(z[nt][2 + c] - ref) : 0.f;
+        l[nt][c] += in0 ? w[c] * vi[0] : 0.f;
+        l[nt][c] += in1 ? w[2 + c] * vi[1] : 0.f;
+      }
+      pb0[nt] = movmatrix_trans(pack_h2(w[0], w[1]));
+      pb1[nt] = movmatrix_trans(pack_h2(w[2], w[3]));
+    }
+
+    // sums: rows = dims, columns = heads, k = tokens
+    const uint32_t *v0 = &vc[0].x, *v1 = &vc[1].x, *v2 = &vc[2].x,
+                   *v3 = &vc[3].x;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const uint32_t a01 = byte_perm(v0[w], v1[w], 0x5140);
+      const uint32_t a23 = byte_perm(v2[w], v3[w], 0x5140);
+      const uint32_t b01 = byte_perm(v0[w], v1[w], 0x7362);
+      const uint32_t b23 = byte_perm(v2[w], v3[w], 0x7362);
+      const uint32_t fa[4] = {e4m3x2_lo(a01), e4m3x2_hi(a01), e4m3x2_lo(a23),
+                              e4m3x2_hi(a23)};
+      const uint32_t fb[4] = {e4m3x2_lo(b01), e4m3x2_hi(b01), e4m3x2_lo(b23),
+                              e4m3x2_hi(b23)};
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        mma_f16(o[nt][2 * w], fa, pb0[nt], pb1[nt]);
+        mma_f16(o[nt][2 * w + 1], fb, pb0[nt], pb1[nt]);
+      }
+    }
+
+    // the stage is read: refill it
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i + 1 < kQdStages; ++i) {
+      fn[i] = fn[i + 1];
+      fu[i] = fu[i + 1];
+    }
+    int phys;
+    fn[kQdStages - 1] = fu[kQdStages - 1] = 0;
+    next(phys, fn[kQdStages - 1], fu[kQdStages - 1]);
+    if (phys < 0)
+      fn[kQdStages - 1] = 0;
+    else
+      issue(st, phys, fu[kQdStages - 1]);
+    if (++st == kQdStages) {
+      st = 0;
+      phase ^= 1;
+    }
+  }
+  if (dead) {  // give the copies in flight a last, bounded chance to land
+    if (lane == 0) set_status(a.status, LOCKS_DEV_TIMEOUT);
+    for (int i = 0; i < kQdStages; ++i) {
+      mbar_wait(bar + i, 0, 1u << 16);
+      mbar_wait(bar + i, 1, 1u << 16);
+    }
+  }
+  __syncwarp();
+
+  if constexpr (!UNIT) {
+    const int last = lists.unit(pe - 1);
+    advance(last);
+    flush(last);
+  } else {
+    // the 4 C slices of the unit, merged head by head: CTA r of the cluster
+    // takes heads r, r + C, .., its warp w every fourth of those; a lane
+    // four dims
+    flush(unit0);
+    if (ucl > 1)
+      cluster_sync();
+    else
+      __syncthreads();
+    const int b = unit0 / a.h_kv, h = unit0 - b * a.h_kv;
+    const int nsl = ucl * kQdWarps;
+    const uint32_t base = smem_u32(smem);
+    auto part = [&](int sl, int byte) -> uint32_t {
+      const uint32_t at =
+          base + (uint32_t)((sl % kQdWarps) * kQdWarpRing + byte);
+      return ucl > 1 ? mapa_shared(at, (uint32_t)(sl / kQdWarps)) : at;
+    };
+    constexpr int kOffMl = 8 * NT * kDim * 4;
+    for (int hd = urank + ucl * wid; hd < a.G; hd += ucl * kQdWarps) {
+      // lane sl holds slice sl's reference and sum (at most 32 slices)
+      float pm = -INFINITY, pl = 0.f;
+      if (lane < nsl) {
+        const uint32_t at = part(lane, kOffMl + 8 * hd);
+        pm = ld_cluster_f32(at);
+        pl = ld_cluster_f32(at + 4);
+      }
+      float M = pm;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1)
+        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+      // a slice without tokens weighs nothing; one whose scores are not
+      // numbers carries that on
+      const float wt = pl == 0.f || pm == M ? (pl == 0.f ? 0.f : 1.f)
+                                            : ex2_fast(pm - M);
+      float sum = pl * wt;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1)
+        sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int s0 = 0; s0 < nsl; s0 += 4) {
+        float4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          v[i] = ld_cluster_v4f(part(s0 + i, (hd * kDim + 4 * lane) * 4));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x = __shfl_sync(0xffffffffu, wt, s0 + i);
+          if (x == 0.f) continue;
+          acc.x = fmaf(x, v[i].x, acc.x);
+          acc.y = fmaf(x, v[i].y, acc.y);
+          acc.z = fmaf(x, v[i].z, acc.z);
+          acc.w = fmaf(x, v[i].w, acc.w);
+        }
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const size_t row = (size_t)b * h_q + (size_t)h * a.G + hd;
+      reinterpret_cast<uint2 *>(a.o_out + row * kDim)[lane] =
+          make_uint2(pack_bf2q(acc.x * inv, acc.y * inv),
+                     pack_bf2q(acc.z * inv, acc.w * inv));
+      if (lane == 0)
+        a.lse_out[row] = sum == 0.f
+                             ? -INFINITY
+                             : (log2f(sum) + (M - kQdLift)) * kQdLn2;
+    }
+    if (ucl > 1) cluster_sync();  // no CTA leaves while its slices are read
+  }
+}
+
+// ---------------------------------------------------------------------------
+// merge of partials
+// ---------------------------------------------------------------------------
+// One warp per (sequence, query head) row, four dims to a lane: the pieces
+// that the runs left of the row's unit, and before them the partials of the
+// shared prefix where there is one (`shared` of them, [split][batch * h_q],
+// skipped by sequences shorter than the prefix).  Eight partials' loads are
+// in flight at a time.
+constexpr int kMergeWarps = 4;
+constexpr int kMergeGroup = 8;
+
+__global__ void __launch_bounds__(32 * kMergeWarps)
+    merge_kernel(const QdArgs a, const float *__restrict__ shared_o,
+                 const float2 *__restrict__ shared_ml, int shared) {
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const long long rows = (long long)a.batch * a.h_kv * a.G;
+  const long long row =
+      (long long)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+  if (row >= rows) return;
+  const int u = (int)(row / a.G), hd = (int)(row - (long long)u * a.G);
+  const int b = u / a.h_kv;
+  const PageLists lists{a.meta + 1, a.batch, a.h_kv,
+                        a.idx ? a.h_kv * a.k : 0};
+  const int chunk = a.meta[0];
+  const int2 sp = lists.span(u);
+  int w0 = 0, own = 0;
+  if (sp.y > sp.x) {
+    w0 = sp.x / chunk;
+    own = (sp.y - 1) / chunk - w0 + 1;
+    if (own == 1 && !a.prefix_pages) return;  // written by its warp
+  }
+  if (shared) {
+    const int L = checked_len(a.seq_lens, b, a.max_pages, nullptr);
+    if (L < a.prefix_pages * kPage) shared = 0;
+  }
+  const int n = shared + own;
+  float M = -INFINITY, sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < n; s0 += kMergeGroup) {
+    float2 ml[kMergeGroup];
+    float4 v[kMergeGroup];
+#pragma unroll
+    for (int i = 0; i < kMergeGroup; ++i) {
+      const int s = s0 + i;
+      ml[i] = make_float2(-INFINITY, 0.f);
+      v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (s >= n) continue;
+      const size_t at = s < shared
+                            ? (size_t)s * rows + row
+                            : ((size_t)u + w0 + (s - shared)) * a.G + hd;
+      ml[i] = (s < shared ? shared_ml : a.ml_part)[at];
+      v[i] = reinterpret_cast<const float4 *>(s < shared ? shared_o
+                                                         : a.o_part)
+                 [at * (kDim / 4) + lane];
+    }
+    float top = M;
+#pragma unroll
+    for (int i = 0; i < kMergeGroup; ++i) top = fmaxf(top, ml[i].x);
+    const float fall = M == top ? 1.f : ex2_fast(M - top);
+    M = top;
+    sum *= fall;
+    acc.x *= fall;
+    acc.y *= fall;
+    acc.z *= fall;
+    acc.w *= fall;
+#pragma unroll
+    for (int i = 0; i < kMergeGroup; ++i) {
+      if (ml[i].y == 0.f) continue;  // no tokens
+      const float x = ml[i].x == M ? 1.f : ex2_fast(ml[i].x - M);
+      sum = fmaf(x, ml[i].y, sum);
+      acc.x = fmaf(x, v[i].x, acc.x);
+      acc.y = fmaf(x, v[i].y, acc.y);
+      acc.z = fmaf(x, v[i].z, acc.z);
+      acc.w = fmaf(x, v[i].w, acc.w);
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  reinterpret_cast<uint2 *>(a.o_out + row * kDim)[lane] = make_uint2(
+      pack_bf2q(acc.x * inv, acc.y * inv), pack_bf2q(acc.z * inv, acc.w * inv));
+  if (lane == 0)
+    a.lse_out[row] =
+        sum == 0.f ? -INFINITY : (log2f(sum) + (M - kQdLift)) * kQdLn2;
+}
+
+// ---------------------------------------------------------------------------
+// launchers
+// ---------------------------------------------------------------------------
+static size_t qdecode_smem(bool unit, int batch) {
+  return (size_t)kQdRing + (unit ? 0 : sizeof(int) * ((size_t)batch + 1));
+}
+
+int qdecode_max_batch() {
+  return (int)((227 * 1024 - (size_t)kQdRing - 512) / sizeof(int));
+}
+
+template <int NT, bool UNIT>
+static cudaError_t qdecode_ready() {
+  static DeviceFlags done;
+  return once_per_device(done, [] {
+    return cudaFuncSetAttribute(qdecode_kernel<NT, UNIT>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                226 * 1024);
+  });
+}
+
+// The cluster size of the unit form, 0 for the split form.
+static int unit_cluster(long long units, int k) {
+  const int sms = device_sm_count();
+  if (units > 0x7fffffffLL / (8 * kQdWarps)) return 0;
+  if (units >= sms) return 1;
+  for (int c = 8; c >= 2; c >>= 1)
+    if (units * c <= 2LL * sms && k >= c * kQdWarps) return c;
+  return 0;
+}
+
+cudaError_t launch_qdecode(const void *q, const void *records,
+                           int64_t num_phys, const int32_t *pt,
+                           const int32_t *seq_lens, const int32_t *idx, int k,
+                           int batch, int h_kv, int G, int max_pages,
+                           const int32_t *prefix, int prefix_pages,
+                           int max_warps, void *o_out, float *lse_out,
+                           float *o_part, float2 *ml_part, int *meta,
+                           const float *shared_o, const float2 *shared_ml,
+                           int shared, int32_t *status, cudaStream_t stream) {
+  QdArgs a{static_cast<const __nv_bfloat16 *>(q),
+           static_cast<const uint8_t *>(records),
+           num_phys, pt, seq_lens, idx, k, batch, h_kv, G, max_pages, 0,
+           prefix, prefix_pages, static_cast<__nv_bfloat16 *>(o_out), lse_out,
+           o_part, ml_part, meta, status};
+  const bool wide = G > 8;
+  const long long units = (long long)batch * h_kv;
+  const int ucl = idx ? unit_cluster(units, k) : 0;
+  if (ucl > 0) {
+    cudaError_t e = wide ? qdecode_ready<2, true>() : qdecode_ready<1, true>();
+    if (e != cudaSuccess) return e;
+    auto *kern = wide ? qdecode_kernel<2, true> : qdecode_kernel<1, true>;
+    const dim3 grid((unsigned)(units * ucl));
+    const size_t smem = qdecode_smem(true, batch);
+    return ucl > 1 ? launch_pdl_cluster(kern, grid, dim3(kQdThreads), smem,
+                                        stream, ucl, a)
+                   : launch_pdl(kern, grid, dim3(kQdThreads), smem, stream, a);
+  }
+  cudaError_t e = wide ? qdecode_ready<2, false>() : qdecode_ready<1, false>();
+  if (e != cudaSuccess) return e;
+  // a grid that fills the GPU, at most one warp per list entry
+  long long warps = (long long)(wide ? 2 : 3) * device_sm_count() * kQdWarps;
+  if (warps > max_warps) warps = max_warps;
+  a.n_warps = (int)warps;
+  auto *kern = wide ? qdecode_kernel<2, false> : qdecode_kernel<1, false>;
+  e = launch_pdl(kern, dim3((a.n_warps + kQdWarps - 1) / kQdWarps),
+                 dim3(kQdThreads), qdecode_smem(false, batch), stream, a);
+  if (e != cudaSuccess) return e;
+  const long long rows = units * G;
+  return launch_pdl(merge_kernel,
+                    dim3((unsigned)((rows + kMergeWarps - 1) / kMergeWarps)),
+                    dim3(32 * kMergeWarps), 0, stream, a, shared_o, shared_ml,
+                    shared);
+}
+
+}  // namespace locks
