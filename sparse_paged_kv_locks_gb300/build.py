@@ -25,7 +25,7 @@ LIB = os.path.join(LIBDIR, "liblocks.so")
 SOURCES = ["api.cu", "build.cu", "score.cu", "select.cu", "decode.cu",
            "exact.cu", "variant.cu", "variant_b2.cu", "variant_b4.cu",
            "variant_b8.cu", "noalloc.cu", "decoder.cu", "quantise.cu",
-           "qdecode.cu"]
+           "qdecode.cu", "prefix.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -558,6 +558,24 @@ locks_status_t locks_quantised_decode(
   return e == cudaSuccess ? LOCKS_OK : fail_cuda(e);
 }
 
+// the partials of the shared pages
+struct PrefixRegion {
+  int splits;
+  float *o_part;
+  float2 *ml_part;
+  size_t bytes;
+};
+static PrefixRegion prefix_region(uint8_t *at, int batch, int h_q, int h_kv,
+                                  int pages) {
+  if (pages == 0 || batch == 0) return {0, nullptr, nullptr, 0};
+  const int splits = prefix_splits(batch, h_kv, h_q / h_kv, pages);
+  const size_t rows = (size_t)splits * batch * h_q;
+  const size_t sums = round_up(rows * kDim * 4, 256);
+  return {splits, reinterpret_cast<float *>(at),
+          reinterpret_cast<float2 *>(at + sums),
+          sums + round_up(rows * 8, 256)};
+}
+
 locks_status_t locks_prefix_workspace_size(int batch, int h_q, int h_kv,
                                            int max_pages, int prefix_pages,
                                            size_t *bytes) {
@@ -566,7 +584,8 @@ locks_status_t locks_prefix_workspace_size(int batch, int h_q, int h_kv,
     return LOCKS_ERR_INVALID_ARG;
   if (h_q / h_kv > kMaxGroup) return LOCKS_ERR_UNSUPPORTED;
   *bytes =
-      kWsHeader + qdecode_region(nullptr, batch, h_q, h_kv, max_pages).bytes;
+      kWsHeader + qdecode_region(nullptr, batch, h_q, h_kv, max_pages).bytes +
+      prefix_region(nullptr, batch, h_q, h_kv, prefix_pages).bytes;
   return LOCKS_OK;
 }
 
@@ -587,13 +606,24 @@ locks_status_t locks_prefix_decode(
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   const DecodeRegion r =
       qdecode_region(ws + kWsHeader, batch, h_q, h_kv, max_pages);
-  if (workspace_bytes < kWsHeader + r.bytes) return LOCKS_ERR_WORKSPACE;
-  cudaError_t e = launch_qdecode(
-      q, records, num_phys_pages, page_table, seq_lens, nullptr, 0, batch,
-      h_kv, h_q / h_kv, max_pages, prefix_table, prefix_pages,
-      (int)decode_warps_cap(batch, h_kv, max_pages), o_out, lse_out, r.o_part,
-      r.ml_part, r.meta, nullptr, nullptr, 0, reinterpret_cast<int32_t *>(ws),
-      (cudaStream_t)stream);
+  const PrefixRegion p = prefix_region(ws + kWsHeader + r.bytes, batch, h_q,
+                                       h_kv, prefix_pages);
+  if (workspace_bytes < kWsHeader + r.bytes + p.bytes)
+    return LOCKS_ERR_WORKSPACE;
+  const int G = h_q / h_kv;
+  int32_t *status = reinterpret_cast<int32_t *>(ws);
+  cudaError_t e = cudaSuccess;
+  if (prefix_pages > 0)
+    e = launch_prefix(q, records, num_phys_pages, prefix_table, prefix_pages,
+                      batch, h_kv, G, p.splits, p.o_part, p.ml_part, status,
+                      (cudaStream_t)stream);
+  if (e == cudaSuccess)
+    e = launch_qdecode(q, records, num_phys_pages, page_table, seq_lens,
+                       nullptr, 0, batch, h_kv, G, max_pages, prefix_table,
+                       prefix_pages,
+                       (int)decode_warps_cap(batch, h_kv, max_pages), o_out,
+                       lse_out, r.o_part, r.ml_part, r.meta, p.o_part,
+                       p.ml_part, p.splits, status, (cudaStream_t)stream);
   return e == cudaSuccess ? LOCKS_OK : fail_cuda(e);
 }
 

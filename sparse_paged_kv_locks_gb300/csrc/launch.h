@@ -178,8 +178,10 @@ cudaError_t launch_dequantise(const void *records, int64_t num_phys, int h_kv,
                               cudaStream_t stream);
 
 // prefix, prefix_pages: pages that every sequence begins with (null, 0:
-// none).  o_part, ml_part, meta: the split form's partials (sums not
-// divided; reference and sum of weights) and position layout.
+// none), left out of the lists of sequences at least that long.  o_part,
+// ml_part, meta: the split form's partials (sums not divided; reference and
+// sum of weights) and position layout; shared_o, shared_ml: `shared` partials
+// of every row, [shared][batch * h_kv * G], for those sequences.
 cudaError_t launch_qdecode(const void *q, const void *records,
                            int64_t num_phys, const int32_t *pt,
                            const int32_t *seq_lens, const int32_t *idx, int k,
@@ -190,6 +192,15 @@ cudaError_t launch_qdecode(const void *q, const void *records,
                            const float *shared_o, const float2 *shared_ml,
                            int shared, int32_t *status, cudaStream_t stream);
 int qdecode_max_batch();
+
+// attention of all query rows over the shared pages, in `splits` partials
+// (prefix.cu)
+int prefix_splits(int batch, int h_kv, int G, int pages);
+cudaError_t launch_prefix(const void *q, const void *records,
+                          int64_t num_phys, const int32_t *table, int pages,
+                          int batch, int h_kv, int G, int splits,
+                          float *o_part, float2 *ml_part, int32_t *status,
+                          cudaStream_t stream);
 
 size_t variant_record_bytes(int rank, int vbits);
 // largest batch whose per-sequence tables fit beside the variant's ring

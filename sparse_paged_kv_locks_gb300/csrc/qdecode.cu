@@ -49,7 +49,9 @@ struct QdArgs {
   int64_t num_phys;
   const int32_t *pt, *seq_lens, *idx;
   int k, batch, h_kv, G, max_pages, n_warps;
-  // pages that every sequence begins with (null, 0: none)
+  // pages that every sequence begins with (null, 0: none); a sequence at
+  // least that long leaves them out of its list, a shorter one finds its
+  // pages there
   const int32_t *prefix;
   int prefix_pages;
   __nv_bfloat16 *o_out;
@@ -62,7 +64,8 @@ struct QdArgs {
 
 // pages of sequence b's own list, for lists that are not given
 __device__ __forceinline__ int own_pages(const QdArgs &a, int L) {
-  return (L + kPage - 1) / kPage;
+  const int n = (L + kPage - 1) / kPage;
+  return L >= a.prefix_pages * kPage ? n - a.prefix_pages : n;
 }
 
 __device__ __forceinline__ QEntry q_resolve(const QdArgs &a,
@@ -86,8 +89,11 @@ __device__ __forceinline__ QEntry q_resolve(const QdArgs &a,
       set_status(a.status, LOCKS_DEV_BAD_INDEX);
       return e;
     }
-  } else if (pg < a.prefix_pages) {
-    table = a.prefix;
+  } else if (a.prefix_pages) {
+    if (L >= a.prefix_pages * kPage)
+      pg += a.prefix_pages;
+    else
+      table = a.prefix;
   }
   const int ph = __ldg(table + pg);
   if (ph < 0 || ph >= a.num_phys) {
