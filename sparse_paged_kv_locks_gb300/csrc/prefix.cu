@@ -5,19 +5,33 @@
 //
 // A CTA takes 128 query rows of a KV head and a range of 128-token tiles.
 // Both products are tcgen05 matrix products with fp32 accumulators in tensor
-// memory: S = Q K^T from shared memory, O += W V with the weights W in fp16
-// in tensor memory over the scores they came from.  Codes are exact in fp16;
-// a page's rows are scaled there by 2^(e - E), E the largest exponent of the
-// page, which is exact for rows within 2^15 of the page's largest (and below
-// that off by 2^-25 of the page's largest code).  2^E of the keys multiplies
-// a page's scores, E of the values joins the weights' exponent.
+// memory: S = Q K^T, O += W V with the weights W in fp16 in tensor memory
+// over the scores they came from.
+//
+// Keys take part as they are stored: the e4m3 rows are copied to shared
+// memory, and the query row is the sum of two e4m3 rows, hi + lo, after a
+// power-of-two scale that puts its largest magnitude in (224, 448].  A bf16
+// number has 8 significant bits, a code 4, so hi + lo is exact down to 2^-11
+// of the row's largest element and off by at most 2^-10, 2^-18 of it, below.
+// A key's scale multiplies its column of scores.  Value codes are widened to
+// fp16, a page's rows scaled by 2^(e - E), E the largest exponent of the
+// page: exact for rows within 2^15 of the page's largest (and below that off
+// by 2^-25 of the page's largest code).  E joins the weights' exponent.
+//
+// Rows of a record are swizzled by f(s) = (s & 6) ^ 5 (s & 1), rows of the
+// tensor core's operand by s & 7.  The two agree on even rows; an odd row's
+// halves trade places in shared memory before its product.
 //
 // Eight warps: 0-3 softmax, a query row to a thread, so that maxima and sums
-// need no exchange; 4-7 bring records from memory and lay the fp16 tiles out
-// for the tensor core, and one thread of theirs issues the products.  K and
-// V have one tile buffer each: the values of tile j and the keys of j + 1 are
-// laid out while the softmax of tile j runs.  Two CTAs fit an SM, and one's
-// softmax runs under the other's products.
+// need no exchange; 4 has the records copied (two bulk copies a page: keys;
+// values with all scales) and issues the products; 5-7 mend the keys and
+// widen the values.  A buffer's next copy starts when it has been read.  Two
+// CTAs fit an SM, and one's softmax runs under the other's products.
+//
+// (Loads to registers instead of bulk copies stalled their warps for 2000 to
+// 3000 cycles a tile: the pages lie far apart, and the proxy fence before a
+// product waits for its thread's loads.  Copies of single rows to their
+// swizzled places took 7000 cycles a tile to issue.)
 #include "launch.h"
 #include "quantised.cuh"
 
@@ -27,9 +41,12 @@ constexpr int kPfRows = 128;   // query rows of a CTA
 constexpr int kPfTile = 128;   // tokens of a tile
 constexpr int kPfPages = kPfTile / kPage;
 constexpr int kPfThreads = 256;
-constexpr int kPfOperand = kPfRows * kDim * 2;  // an fp16 tile, 32 KB
-constexpr int kPfBlock = kPfOperand / 2;        // its half of 64 dims
-constexpr int kPfSmem = 3 * kPfOperand + 1024;
+constexpr int kPfWiden = 3;    // warps that mend keys and widen values
+constexpr int kPfCodes = kPfTile * kDim;    // a tile of e4m3 rows, 16 KB
+constexpr int kPfBlock = kPfTile * 128;     // 64 dims of an fp16 tile, 16 KB
+constexpr int kPfRest = kQRec - kQOffV;     // values and scales of a record
+constexpr int kPfSmem =
+    3 * kPfCodes + 2 * kPfBlock + kPfPages * kPfRest + 1024;
 constexpr int kPfColumns = 256;                 // tensor memory: S, O
 constexpr int kPfColO = 128;
 constexpr float kPfScale = 0.12751743074602467f;  // log2(e) / sqrt(128)
@@ -48,7 +65,8 @@ __device__ __forceinline__ uint64_t mat_desc(uint32_t addr, uint32_t lead) {
   return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(lead >> 4) << 16 |
          (uint64_t)(1024u >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
-// fp16 x fp16 -> fp32, M = N = 128; bit 16: B runs along N
+// fp32 accumulators, operands of format 0 (e4m3 of kind::f8f6f4, fp16 of
+// kind::f16), M = N = 128; bit 16: B runs along N
 constexpr uint32_t kPfDescS =
     1u << 4 | (128u >> 3) << 17 | (128u >> 4) << 24;
 constexpr uint32_t kPfDescO = kPfDescS | 1u << 16;
@@ -57,7 +75,7 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b,
                                        uint32_t desc, bool add) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
       "l"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
       : "memory");
 }
@@ -120,6 +138,17 @@ __device__ __forceinline__ void tm_st32(uint32_t addr,
       : "memory");
 }
 // 16 columns
+__device__ __forceinline__ void tm_ld16(uint32_t (&r)[16], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]),
+        "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
 __device__ __forceinline__ void tm_st16(uint32_t addr,
                                         const uint32_t (&r)[16]) {
   asm volatile(
@@ -146,6 +175,51 @@ __device__ __forceinline__ void st_shared_v4(uint32_t a, uint4 v) {
                : "memory");
 }
 
+// two fp32 numbers in one 64-bit register pair
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  return pack2(__float_as_uint(lo), __float_as_uint(hi));
+}
+__device__ __forceinline__ float2 unpack2(uint64_t x) {
+  uint32_t lo, hi;
+  asm("mov.b64 {%0, %1}, %2;\n" : "=r"(lo), "=r"(hi) : "l"(x));
+  return make_float2(__uint_as_float(lo), __uint_as_float(hi));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// bytes from global memory to shared address `to`
+__device__ __forceinline__ void bulk_rows(uint32_t to, const void *from,
+                                          uint32_t bytes, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1], %2, [%3];\n" ::"r"(to),
+      "l"(from), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // byte offset of 16-byte chunk c (0..15, 8 fp16 each) of row r in a tile:
 // two blocks of 64 dims, rows of 128 bytes, chunks swizzled by the row
 __device__ __forceinline__ uint32_t tile_at(int r, int c) {
@@ -165,13 +239,14 @@ struct PfArgs {
 };
 
 struct PfShared {
-  uint64_t k_full, v_full, p_full, qk_done, pv_done, drain;
+  // of the tile whose scores are being taken: scales of the keys, E and 2^-E
+  // of the pages' values, and which pages are there
+  float k_scale[kPfTile];
+  float v_exp[kPfPages], v_inv[kPfPages];
+  uint32_t there;
   uint32_t tmem;
   int dead;
-  // per tile parity and page: 2^E of the keys, E and 2^-E of the values,
-  // and which pages are there
-  float k_scale[2][kPfPages], v_exp[2][kPfPages], v_inv[2][kPfPages];
-  uint32_t there[2];
+  uint64_t k_raw, v_raw, k_full, v_full, info, p_full, qk_done, pv_done, drain;
 };
 
 // false when the wait gave up, or some other thread's did
@@ -192,7 +267,9 @@ __global__ void __launch_bounds__(kPfThreads, 2)
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   // swizzled tiles start at multiples of 1024 bytes
   const uint32_t q_s = (smem_u32(raw_smem) + 1023u) & ~1023u;
-  const uint32_t k_s = q_s + kPfOperand, v_s = k_s + kPfOperand;
+  const uint32_t k_s = q_s + 2 * kPfCodes;
+  const uint32_t v_s = k_s + kPfCodes;
+  const uint32_t raw_s = v_s + 2 * kPfBlock;  // [page][kPfRest]
 
   // this CTA's KV head, query rows and tiles
   const int tiles = (a.pages + kPfPages - 1) / kPfPages;
@@ -213,8 +290,11 @@ __global__ void __launch_bounds__(kPfThreads, 2)
         "r"(kPfColumns)
         : "memory");
     if (lane == 0) {
-      mbar_init(&sh.k_full, 4);
-      mbar_init(&sh.v_full, 4);
+      mbar_init(&sh.k_raw, 1);
+      mbar_init(&sh.v_raw, 1);
+      mbar_init(&sh.info, kPfWiden);
+      mbar_init(&sh.k_full, kPfWiden);
+      mbar_init(&sh.v_full, kPfWiden);
       mbar_init(&sh.p_full, 4);
       mbar_init(&sh.qk_done, 1);
       mbar_init(&sh.pv_done, 1);
@@ -226,42 +306,54 @@ __global__ void __launch_bounds__(kPfThreads, 2)
   pdl_wait();
   pdl_trigger();
 
-  // the query rows, fp16, each scaled so that its largest magnitude lies in
-  // [2^7, 2^8)
+  // the query rows: hi and lo codes, the scale that they leave to scores
   float f = 0.f;
   if (wid < 4) {
-    uint32_t w[64];
-    if (row < rows) {
-      const uint4 *src = reinterpret_cast<const uint4 *>(
-          a.q + ((size_t)(row / a.G) * a.h_kv * a.G + (size_t)h * a.G +
-                 row % a.G) * kDim);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const uint4 v = __ldg(src + i);
-        w[4 * i] = v.x;
-        w[4 * i + 1] = v.y;
-        w[4 * i + 2] = v.z;
-        w[4 * i + 3] = v.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 64; ++i) w[i] = 0u;
-    }
+    const uint4 *src = reinterpret_cast<const uint4 *>(
+        a.q + ((size_t)(row / a.G) * a.h_kv * a.G + (size_t)h * a.G +
+               row % a.G) * kDim);
+    const bool in = row < rows;
     float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < 64; ++i)
-      top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
-    const int e = max(-100, (int)(__float_as_uint(top) >> 23) - 127) - 7;
+    for (int i = 0; i < 16; ++i) {
+      const uint4 v = in ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+      const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        top = fmaxf(top, fmaxf(fabsf(bf16_lo(x[k])), fabsf(bf16_hi(x[k]))));
+    }
+    // least e with top <= 448 * 2^e
+    const uint32_t tb = __float_as_uint(top);
+    const int e =
+        max(-100, (int)(tb >> 23) - 135 + ((tb & 0x7fffffu) > 0x600000u));
     const float down = exp2_int(-e);
     f = exp2_int(e) * kPfScale;
+#pragma unroll 2
+    for (int i = 0; i < 8; ++i) {  // 16 dims
+      uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      uint32_t x[4];
+      for (int k = 0; k < 2; ++k) {
+        const uint4 v =
+            in ? __ldg(src + 2 * i + k) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        x[j] = h2_as_u32(__floats2half2_rn(bf16_lo(w[4 * i + j]) * down,
-                                           bf16_hi(w[4 * i + j]) * down));
-      st_shared_v4(q_s + tile_at(tid, i), make_uint4(x[0], x[1], x[2], x[3]));
+        for (int n2 = 0; n2 < 2; ++n2) {
+          const float a0 = bf16_lo(x[2 * n2]) * down;
+          const float a1 = bf16_hi(x[2 * n2]) * down;
+          const float a2 = bf16_lo(x[2 * n2 + 1]) * down;
+          const float a3 = bf16_hi(x[2 * n2 + 1]) * down;
+          const uint32_t c =
+              e4m3x2_from(a0, a1) | e4m3x2_from(a2, a3) << 16;
+          const float2 h0 = __half22float2(u32_as_h2(e4m3x2_lo(c)));
+          const float2 h1 = __half22float2(u32_as_h2(e4m3x2_hi(c)));
+          hi[2 * k + n2] = c;
+          lo[2 * k + n2] = e4m3x2_from(a0 - h0.x, a1 - h0.y) |
+                           e4m3x2_from(a2 - h1.x, a3 - h1.y) << 16;
+        }
+      }
+      const uint32_t at = q_s + tid * 128 + ((i ^ (tid & 7)) << 4);
+      st_shared_v4(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+      st_shared_v4(at + kPfCodes, make_uint4(lo[0], lo[1], lo[2], lo[3]));
     }
     fence_to_async();
   }
@@ -276,81 +368,98 @@ __global__ void __launch_bounds__(kPfThreads, 2)
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < n && ok; ++j) {
-      ok = pf_wait(sh, &sh.qk_done, j & 1);
+      ok = pf_wait(sh, &sh.qk_done, j & 1) && pf_wait(sh, &sh.info, j & 1);
       // all products before S(j), among them O(j - 1), are done
       if (ok && j > 0) ok = pf_wait(sh, &sh.pv_done, (j - 1) & 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tm_fence_after();
-      const int par = j & 1;
-      const uint32_t there = sh.there[par];
-      // largest score plus value exponent of the row
-      float top = -INFINITY;
+      const uint32_t there = sh.there;
+      // 64 columns: their weights go over the scores they come from, in
+      // columns that have been read
+      for (int c = 0; c < 2; ++c) {
+        uint64_t x[32];
+        {
+          uint32_t s0[32], s1[32];
+          tm_ld32(s0, mine + 64 * c);
+          tm_ld32(s1, mine + 64 * c + 32);
+          tm_wait_ld();
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t s[32];
-        tm_ld32(s, mine + 32 * c);
-        tm_wait_ld();
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          float x = __uint_as_float(s[16 * p]);
-#pragma unroll
-          for (int i = 1; i < 16; ++i)
-            x = fmaxf(x, __uint_as_float(s[16 * p + i]));
-          const int pg = 2 * c + p;
-          if (there >> pg & 1)
-            top = fmaxf(top, fmaf(x, f * sh.k_scale[par][pg],
-                                  sh.v_exp[par][pg]));
-        }
-      }
-      const bool raise = top > m + kPfSlack;
-      if (__any_sync(0xffffffffu, raise)) {
-        const float to = raise ? top : m;
-        const float fall = to == m ? 1.f : ex2_fast(m - to);
-        m = to;
-        l *= fall;
-        if (j > 0) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t o[32];
-            tm_ld32(o, mine + kPfColO + 32 * c);
-            tm_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              o[i] = __float_as_uint(__uint_as_float(o[i]) * fall);
-            tm_st32(mine + kPfColO + 32 * c, o);
+          for (int i = 0; i < 16; ++i) {
+            x[i] = pack2(s0[2 * i], s0[2 * i + 1]);
+            x[16 + i] = pack2(s1[2 * i], s1[2 * i + 1]);
           }
         }
-      }
-      // weights, over the scores they come from
+        float top = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t s[32], w[16];
-        tm_ld32(s, mine + 32 * c);
-        tm_wait_ld();
+        for (int p = 0; p < 4; ++p) {
+          const int pg = 4 * c + p;
+          float t4[4];
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const int pg = 2 * c + p;
-          if (there >> pg & 1) {
-            const float mul = f * sh.k_scale[par][pg];
-            const float add = sh.v_exp[par][pg] - (m - kPfLift);
-            float sum = 0.f;
+          for (int i = 0; i < 4; ++i) {
+            const float4 k4 =
+                reinterpret_cast<const float4 *>(sh.k_scale)[4 * pg + i];
+            uint64_t &x0 = x[8 * p + 2 * i], &x1 = x[8 * p + 2 * i + 1];
+            x0 = mul2(x0, pack2(k4.x, k4.y));
+            x1 = mul2(x1, pack2(k4.z, k4.w));
+            const float2 u = unpack2(x0), v = unpack2(x1);
+            t4[i] = fmaxf(max3(u.x, u.y, v.x), v.y);
+          }
+          const float t1 = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]);
+          if (there >> pg & 1) top = fmaxf(top, fmaf(t1, f, sh.v_exp[pg]));
+        }
+        const bool raise = top > m + kPfSlack;
+        if (__any_sync(0xffffffffu, raise)) {  // rare after the first tiles
+          const float to = raise ? top : m;
+          const float fall = to == m ? 1.f : ex2_fast(m - to);
+          m = to;
+          l *= fall;
+          tm_wait_st();
+          for (int k = 0; k < 2 * c; ++k) {  // this tile's weights so far
+            uint32_t w[16];
+            tm_ld16(w, mine + 16 * k);
+            tm_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float x = ex2_fast(
-                  fmaf(__uint_as_float(s[16 * p + 2 * i]), mul, add));
-              const float y = ex2_fast(
-                  fmaf(__uint_as_float(s[16 * p + 2 * i + 1]), mul, add));
-              sum += x + y;
-              w[8 * p + i] = h2_as_u32(__floats2half2_rn(x, y));
+            for (int i = 0; i < 16; ++i) {
+              const float2 v = __half22float2(u32_as_h2(w[i]));
+              w[i] = h2_as_u32(__floats2half2_rn(v.x * fall, v.y * fall));
             }
-            l = fmaf(sum, sh.v_inv[par][pg], l);
+            tm_st16(mine + 16 * k, w);
+          }
+          for (int k = 0; k < 8 && j > 0; ++k) {
+            uint32_t o[16];
+            tm_ld16(o, mine + kPfColO + 16 * k);
+            tm_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              o[i] = __float_as_uint(__uint_as_float(o[i]) * fall);
+            tm_st16(mine + kPfColO + 16 * k, o);
+          }
+        }
+        uint32_t w[32];
+        const uint64_t ff = pack2(f, f);
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const int pg = 4 * c + p;
+          const float add = sh.v_exp[pg] - (m - kPfLift);
+          const uint64_t aa = pack2(add, add);
+          uint64_t sum[2] = {0, 0};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float2 z = unpack2(fma2(x[8 * p + i], ff, aa));
+            const float u = ex2_fast(z.x), v = ex2_fast(z.y);
+            sum[i & 1] = add2(sum[i & 1], pack2(u, v));
+            w[8 * p + i] = h2_as_u32(__floats2half2_rn(u, v));
+          }
+          if (there >> pg & 1) {
+            const float2 t2 = unpack2(add2(sum[0], sum[1]));
+            l = fmaf(t2.x + t2.y, sh.v_inv[pg], l);
           } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) w[8 * p + i] = 0u;
           }
         }
-        tm_st16(mine + 16 * c, w);
+        tm_st32(mine + 32 * c, w);
       }
       tm_wait_st();
       tm_fence_before();
@@ -364,7 +473,6 @@ __global__ void __launch_bounds__(kPfThreads, 2)
     const size_t at = (size_t)split * all +
                       (size_t)(row / a.G) * a.h_kv * a.G + (size_t)h * a.G +
                       row % a.G;
-#pragma unroll
     for (int c = 0; c < 4; ++c) {
       uint32_t o[32];
       tm_ld32(o, mine + kPfColO + 32 * c);
@@ -381,135 +489,60 @@ __global__ void __launch_bounds__(kPfThreads, 2)
     }
     if (row < rows) a.ml_part[at] = make_float2(m, ok ? l : 0.f);
   } else {
-    // --------------------------------------------- fp16 operands, products
-    // thread i moves the 16-byte group i of every page's key or value codes:
-    // slot s, dims 16 c .. 16 c + 15
-    const int i = tid - 128, s = i >> 3, warp = wid - 4;
-    const int c = q_group(i & 7, s);
-    uint4 kraw[kPfPages], vraw[kPfPages];
-    uint4 ksc, vsc, vsc_next;  // scale bytes of page lane & 7
-    bool there = false;
-    auto page = [&](int t) -> int {  // page lane & 7 of tile t
+    auto good = [&](int ph) -> bool { return ph >= 0 && ph < a.num_phys; };
+    // page lane & 7 of tile t as the table has it, -1 past the end
+    auto page = [&](int t) -> int {
       const int pg = t * kPfPages + (lane & 7);
-      if (t >= t1 || pg >= a.pages) return -1;
-      const int ph = __ldg(a.table + pg);
-      if (ph >= 0 && ph < a.num_phys) return ph;
-      set_status(a.status, LOCKS_DEV_BAD_PAGE_ID);
-      return -1;
+      return t < t1 && pg < a.pages ? __ldg(a.table + pg) : -1;
     };
-    auto load = [&](int ph, int off, uint4 (&raw)[kPfPages]) {
-#pragma unroll
-      for (int p = 0; p < kPfPages; ++p) {
-        const int php = __shfl_sync(0xffffffffu, ph, p);
-        raw[p] = make_uint4(0u, 0u, 0u, 0u);
-        if (php >= 0)
-          raw[p] = __ldg(reinterpret_cast<const uint4 *>(
-              a.records + ((size_t)php * a.h_kv + h) * kQRec + off + 16 * i));
-      }
+    auto pages_there = [&](int ph) -> uint32_t {
+      return __ballot_sync(0xffffffffu, good(ph)) & 0xffu;
     };
-    auto load_scales = [&](int ph, uint4 &ks, uint4 &vs) {
-      ks = vs = make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
-      if (ph >= 0) {
-        const uint4 *sc = reinterpret_cast<const uint4 *>(
-            a.records + ((size_t)ph * a.h_kv + h) * kQRec + kQOffKE);
-        ks = __ldg(sc);
-        vs = __ldg(sc + 1);
-      }
-    };
-    auto top_byte = [&](uint4 x) -> uint32_t {
-      uint32_t b = __vmaxu4(__vmaxu4(x.x, x.y), __vmaxu4(x.z, x.w));
-      b = __vmaxu4(b, b >> 16);
-      return max(b & 0xffu, b >> 8 & 0xffu);
-    };
-    auto store = [&](const uint4 (&raw)[kPfPages], uint4 sc, uint32_t ref,
-                     uint32_t base) {
-      // the scale bytes of slots 4 warp .. 4 warp + 3
-      const uint32_t four = warp == 0 ? sc.x : warp == 1 ? sc.y
-                            : warp == 2 ? sc.z : sc.w;
-#pragma unroll
-      for (int p = 0; p < kPfPages; ++p) {
-        const uint32_t er = __shfl_sync(0xffffffffu, ref, p);
-        const uint32_t e =
-            __shfl_sync(0xffffffffu, four, p) >> (8 * (lane >> 3)) & 0xffu;
-        // 2^(e - E): exact down to 2^-24, zero below
-        const __half2 x =
-            __float2half2_rn(exp2_int(max(-126, (int)e - (int)er)));
-        const uint32_t w[4] = {raw[p].x, raw[p].y, raw[p].z, raw[p].w};
-        uint32_t y[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          y[2 * k] = h2_as_u32(__hmul2(u32_as_h2(e4m3x2_lo(w[k])), x));
-          y[2 * k + 1] = h2_as_u32(__hmul2(u32_as_h2(e4m3x2_hi(w[k])), x));
-        }
-        const int r = p * kPage + s;
-        st_shared_v4(base + tile_at(r, 2 * c),
-                     make_uint4(y[0], y[1], y[2], y[3]));
-        st_shared_v4(base + tile_at(r, 2 * c + 1),
-                     make_uint4(y[4], y[5], y[6], y[7]));
-      }
-    };
-    const bool issuer = warp == 0 && lane == 0;
-    // keys of tile j from kraw, with the tile's scale references
-    auto store_keys = [&](int j) {
-      const uint32_t kref = top_byte(ksc), vref = top_byte(vsc_next);
-      store(kraw, ksc, kref, k_s);
-      const uint32_t mask = __ballot_sync(0xffffffffu, there) & 0xffu;
-      if (warp == 0) {
-        const int par = j & 1;
-        if (lane < kPfPages) {
-          sh.k_scale[par][lane] = exp2_int((int)kref - 127);
-          sh.v_exp[par][lane] = (float)((int)vref - 127);
-          sh.v_inv[par][lane] = exp2_int(127 - (int)vref);
-        }
-        if (lane == 0) sh.there[par] = mask;
-      }
-      fence_to_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.k_full);
-    };
-    int ph = page(t0);
-    load(ph, 0, kraw);
-    load(ph, kQOffV, vraw);
-    load_scales(ph, ksc, vsc_next);
-    there = ph >= 0;
-    store_keys(0);
+    int ph = page(t0), ph_next = page(t0 + 1);
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      if (issuer) {
+    if (wid == 4) {
+      // ---------------------------------------------- copies and products
+      auto copy = [&](int ph, int off, uint32_t bytes, uint32_t to,
+                      uint64_t *bar) {
+        const uint32_t there = pages_there(ph);
+        if (lane == 0) mbar_arrive_tx(bar, __popc(there) * bytes);
+        __syncwarp();
+        if (lane < kPfPages && (there >> lane & 1))
+          bulk_rows(to + lane * bytes,
+                    a.records + ((size_t)ph * a.h_kv + h) * kQRec + off,
+                    bytes, bar);
+      };
+      copy(ph, 0, kQCodes, k_s, &sh.k_raw);
+      copy(ph, kQOffV, kPfRest, raw_s, &sh.v_raw);
+      for (int j = 0; j < n; ++j) {
+        if (lane < kPfPages && !good(ph) &&
+            (t0 + j) * kPfPages + lane < a.pages)
+          set_status(a.status, LOCKS_DEV_BAD_PAGE_ID);
         ok = pf_wait(sh, &sh.k_full, j & 1);
-        if (ok) {
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (lane == 0) {
           tm_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t off = (kk >> 2) * kPfBlock + (kk & 3) * 32;
-            mma_ss(tm, mat_desc(q_s + off, 16), mat_desc(k_s + off, 16),
-                   kPfDescS, kk > 0);
-          }
+          for (int kk = 0; kk < 8; ++kk)  // hi, then lo
+            mma_ss(tm,
+                   mat_desc(q_s + (kk >> 2) * kPfCodes + (kk & 3) * 32, 16),
+                   mat_desc(k_s + (kk & 3) * 32, 16), kPfDescS, kk > 0);
           mma_commit(&sh.qk_done);
         }
-      }
-      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-      vsc = vsc_next;
-      const uint32_t vref = top_byte(vsc);
-      ph = page(t0 + j + 1);
-      load(ph, 0, kraw);
-      load_scales(ph, ksc, vsc_next);
-      there = ph >= 0;
-      ok = j == 0 || pf_wait(sh, &sh.pv_done, (j - 1) & 1);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      store(vraw, vsc, vref, v_s);
-      fence_to_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.v_full);
-      load(ph, kQOffV, vraw);
-      if (j + 1 < n) {
-        ok = pf_wait(sh, &sh.qk_done, j & 1);
+        __syncwarp();
+        if (j + 1 < n) {  // S(j) done: its keys may go; values likewise
+          ok = pf_wait(sh, &sh.qk_done, j & 1);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          copy(ph_next, 0, kQCodes, k_s, &sh.k_raw);
+        }
+        ok = pf_wait(sh, &sh.v_full, j & 1);
         if (!__all_sync(0xffffffffu, ok)) break;
-        store_keys(j + 1);
-      }
-      if (issuer) {
-        ok = pf_wait(sh, &sh.v_full, j & 1) && pf_wait(sh, &sh.p_full, j & 1);
-        if (ok) {
+        if (j + 1 < n) copy(ph_next, kQOffV, kPfRest, raw_s, &sh.v_raw);
+        ph = ph_next;
+        ph_next = page(t0 + j + 2);
+        ok = pf_wait(sh, &sh.p_full, j & 1);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (lane == 0) {
           tm_fence_after();
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
@@ -518,15 +551,138 @@ __global__ void __launch_bounds__(kPfThreads, 2)
                    j > 0 || kk > 0);
           mma_commit(&sh.pv_done);
         }
+        __syncwarp();
       }
-      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-    }
-    if (issuer && *(volatile int *)&sh.dead) {
-      // give what was issued a last, bounded chance to finish
-      set_status(a.status, LOCKS_DEV_TIMEOUT);
-      mma_commit(&sh.drain);
-      for (uint32_t i2 = 0; i2 < kPfSpin; ++i2)
-        if (mbar_try_wait(&sh.drain, 0)) break;
+      if (lane == 0 && *(volatile int *)&sh.dead) {
+        // give what is in flight a last, bounded chance to finish
+        set_status(a.status, LOCKS_DEV_TIMEOUT);
+        mma_commit(&sh.drain);
+        mbar_wait(&sh.drain, 0, 1u << 16);
+        for (uint32_t k = 0; k < 2; ++k) {
+          mbar_wait(&sh.k_raw, k, 1u << 16);
+          mbar_wait(&sh.v_raw, k, 1u << 16);
+        }
+      }
+    } else {
+      // --------------------------------------------------- keys and values
+      // Warp w takes pages w, w + 3, w + 6 of a tile.  Eight lanes that
+      // read and store a 16-byte group each have the same half of the dims
+      // of slots s and s + 1, which either swizzle keeps in different banks.
+      const int warp = wid - 5;
+      const int s4 = (lane >> 4) * 2 + (lane >> 2 & 1);
+      const int c = (lane & 3) | (lane >> 1 & 4);
+      // the halves of odd key rows trade places
+      auto mend_keys = [&]() {
+        uint4 x[3], y[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          const int pair = 32 * (3 * i + warp) + lane;  // of 256
+          const uint32_t at =
+              k_s + (2 * (pair >> 2) + 1) * 128 + 16 * (pair & 3);
+          if (pair < 256) {
+            x[i] = lds128(at);
+            y[i] = lds128(at + 64);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          const int pair = 32 * (3 * i + warp) + lane;
+          const uint32_t at =
+              k_s + (2 * (pair >> 2) + 1) * 128 + 16 * (pair & 3);
+          if (pair < 256) {
+            st_shared_v4(at, y[i]);
+            st_shared_v4(at + 64, x[i]);
+          }
+        }
+        fence_to_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.k_full);
+      };
+      // Scales of this warp's pages: what softmax needs of them, and the
+      // factors 2^(e - E) of their value rows, exact down to 2^-24 and zero
+      // below.  Lane 16 i + slot: its i-th page, and its third in lanes 0-15.
+      __half2 factor[2];
+      auto tell = [&](uint32_t there) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int pg = warp + 6 * i + 3 * (lane >> 4), sl = lane & 15;
+          const bool in = pg < kPfPages && (there >> pg & 1);
+          uint32_t ek = 127, ev = 127;
+          if (in) {
+            const uint32_t at =
+                raw_s + pg * kPfRest + (kQOffKE - kQOffV) + sl;
+            asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(ek) : "r"(at));
+            asm volatile("ld.shared.u8 %0, [%1];\n"
+                         : "=r"(ev)
+                         : "r"(at + kPage));
+          }
+          uint32_t top = ev;
+#pragma unroll
+          for (int o = 1; o < 16; o <<= 1)
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          if (pg < kPfPages) {
+            sh.k_scale[kPage * pg + sl] = __uint_as_float(ek << 23);
+            if (sl == 0) {
+              sh.v_exp[pg] = (float)((int)top - 127);
+              sh.v_inv[pg] = exp2_int(127 - (int)top);
+            }
+          }
+          factor[i] =
+              __float2half2_rn(exp2_int(max(-126, (int)ev - (int)top)));
+        }
+        if (warp == 0 && lane == 0) sh.there = there;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.info);
+      };
+      auto store_values = [&](uint32_t there) {
+        // all loads first, then page by page
+        uint4 raw[12];
+#pragma unroll
+        for (int u = 0; u < 12; ++u) {  // page u / 4, its slots 4 (u % 4) ..
+          const int p = warp + 3 * (u >> 2), sl = 4 * (u & 3) + s4;
+          raw[u] = p < kPfPages && (there >> p & 1)
+                       ? lds128(raw_s + p * kPfRest + sl * kDim +
+                                16 * q_group(c, sl))
+                       : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int u = 0; u < 12; ++u) {
+          const int p = warp + 3 * (u >> 2), sl = 4 * (u & 3) + s4;
+          const __half2 x = u32_as_h2(
+              __shfl_sync(0xffffffffu, h2_as_u32(factor[u >> 3]),
+                          16 * (u >> 2 & 1) + sl));
+          if (p >= kPfPages) break;
+          const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+          uint32_t y[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            y[2 * k] = h2_as_u32(__hmul2(u32_as_h2(e4m3x2_lo(w[k])), x));
+            y[2 * k + 1] = h2_as_u32(__hmul2(u32_as_h2(e4m3x2_hi(w[k])), x));
+          }
+          const int r = p * kPage + sl;
+          st_shared_v4(v_s + tile_at(r, 2 * c),
+                       make_uint4(y[0], y[1], y[2], y[3]));
+          st_shared_v4(v_s + tile_at(r, 2 * c + 1),
+                       make_uint4(y[4], y[5], y[6], y[7]));
+        }
+        fence_to_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.v_full);
+      };
+      for (int j = 0; j < n; ++j) {
+        ok = pf_wait(sh, &sh.k_raw, j & 1);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        mend_keys();
+        const uint32_t there = pages_there(ph);
+        ph = ph_next;
+        ph_next = page(t0 + j + 2);
+        // O(j - 1) done: its values, and what softmax knew, may go
+        ok = (j == 0 || pf_wait(sh, &sh.pv_done, (j - 1) & 1)) &&
+             pf_wait(sh, &sh.v_raw, j & 1);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tell(there);
+        store_values(there);
+      }
     }
   }
   __syncwarp();
