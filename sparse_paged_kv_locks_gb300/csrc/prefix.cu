@@ -23,15 +23,20 @@
 // halves trade places in shared memory before its product.
 //
 // Eight warps: 0-3 softmax, a query row to a thread, so that maxima and sums
-// need no exchange; 4 has the records copied (two bulk copies a page: keys;
-// values with all scales) and issues the products; 5-7 mend the keys and
-// widen the values.  A buffer's next copy starts when it has been read.  Two
-// CTAs fit an SM, and one's softmax runs under the other's products.
+// need no exchange; 4 issues the products and has the values (with all
+// scales) copied; 5 has the keys copied and mends them; 6 and 7 widen the
+// values.  A buffer's next copy starts when it has been read: the keys of
+// tile j + 1 come and its values are read to registers while the softmax of
+// tile j runs.  Two CTAs fit an SM, with their columns of tensor memory fill
+// it, and one's softmax runs under the other's products.
 //
 // (Loads to registers instead of bulk copies stalled their warps for 2000 to
 // 3000 cycles a tile: the pages lie far apart, and the proxy fence before a
 // product waits for its thread's loads.  Copies of single rows to their
-// swizzled places took 7000 cycles a tile to issue.)
+// swizzled places took 7000 cycles a tile to issue.  Tiles of 64 tokens with two or
+// three buffers of everything, and so the products of one tile under the
+// softmax of the next, were slower, 335 us against 2XX on the 128K prefix:
+// a product reads the query from shared memory for half as many columns.)
 #include "launch.h"
 #include "quantised.cuh"
 
@@ -41,18 +46,19 @@ constexpr int kPfRows = 128;   // query rows of a CTA
 constexpr int kPfTile = 128;   // tokens of a tile
 constexpr int kPfPages = kPfTile / kPage;
 constexpr int kPfThreads = 256;
-constexpr int kPfWiden = 3;    // warps that mend keys and widen values
-constexpr int kPfCodes = kPfTile * kDim;    // a tile of e4m3 rows, 16 KB
-constexpr int kPfBlock = kPfTile * 128;     // 64 dims of an fp16 tile, 16 KB
+constexpr int kPfWiden = 2;    // warps that widen values
+constexpr int kPfQuery = kPfRows * kDim;    // hi or lo of the query, 16 KB
+constexpr int kPfCodes = kPfTile * kDim;    // a tile of e4m3 keys, 16 KB
+constexpr int kPfBlock = kPfTile * 128;     // 64 dims of fp16 values, 16 KB
 constexpr int kPfRest = kQRec - kQOffV;     // values and scales of a record
+constexpr int kPfRaw = kPfPages * kPfRest;  // a tile of them
 constexpr int kPfSmem =
-    3 * kPfCodes + 2 * kPfBlock + kPfPages * kPfRest + 1024;
-constexpr int kPfColumns = 256;                 // tensor memory: S, O
-constexpr int kPfColO = 128;
+    2 * kPfQuery + kPfCodes + 2 * kPfBlock + kPfRaw + 1024;
+constexpr int kPfColumns = 256;             // tensor memory: S, then O
+constexpr int kPfColO = kPfTile;
 constexpr float kPfScale = 0.12751743074602467f;  // log2(e) / sqrt(128)
 constexpr float kPfLift = 8.f;   // as in the single-token kernel
 constexpr float kPfSlack = 7.f;
-constexpr uint32_t kPfSpin = 1u << 21;  // tries before a wait gives up
 
 // ---------------------------------------------------------------------------
 // tcgen05
@@ -66,10 +72,11 @@ __device__ __forceinline__ uint64_t mat_desc(uint32_t addr, uint32_t lead) {
          (uint64_t)(1024u >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 // fp32 accumulators, operands of format 0 (e4m3 of kind::f8f6f4, fp16 of
-// kind::f16), M = N = 128; bit 16: B runs along N
+// kind::f16), M = 128, N = a tile's tokens or the dims; bit 16: B runs along N
 constexpr uint32_t kPfDescS =
-    1u << 4 | (128u >> 3) << 17 | (128u >> 4) << 24;
-constexpr uint32_t kPfDescO = kPfDescS | 1u << 16;
+    1u << 4 | ((uint32_t)kPfTile >> 3) << 17 | (128u >> 4) << 24;
+constexpr uint32_t kPfDescO =
+    1u << 4 | 1u << 16 | ((uint32_t)kDim >> 3) << 17 | (128u >> 4) << 24;
 
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b,
                                        uint32_t desc, bool add) {
@@ -239,24 +246,39 @@ struct PfArgs {
 };
 
 struct PfShared {
-  // of the tile whose scores are being taken: scales of the keys, E and 2^-E
-  // of the pages' values, and which pages are there
-  float k_scale[kPfTile];
-  float v_exp[kPfPages], v_inv[kPfPages];
-  uint32_t there;
+  // of tile j, at j & 1: scales of the keys, E and 2^-E of the pages' values,
+  // and which pages are there
+  float k_scale[2][kPfTile];
+  float v_exp[2][kPfPages], v_inv[2][kPfPages];
+  uint32_t there[2];
   uint32_t tmem;
   int dead;
-  uint64_t k_raw, v_raw, k_full, v_full, info, p_full, qk_done, pv_done, drain;
+  uint64_t k_raw, k_full, v_raw, v_read, v_full, info[2];
+  uint64_t p_full, qk_done, pv_done, drain;
 };
+
+// one lane of the warp, for what a warp does once
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n"
+      " selp.b32 %0, 1, 0, p;\n}\n"
+      : "=r"(r));
+  return r != 0;
+}
 
 // false when the wait gave up, or some other thread's did
 __device__ __forceinline__ bool pf_wait(PfShared &sh, uint64_t *bar,
                                         uint32_t phase) {
-  for (uint32_t i = 0; i < kPfSpin; ++i) {
+  if (mbar_try_wait(bar, phase)) return true;
+  const long long t0 = clock64();
+  while (!*(volatile int *)&sh.dead) {
     if (mbar_try_wait(bar, phase)) return true;
-    if ((i & 255u) == 255u && *(volatile int *)&sh.dead) return false;
+    if (clock64() - t0 > kQWaitCycles) {
+      *(volatile int *)&sh.dead = 1;
+      break;
+    }
   }
-  *(volatile int *)&sh.dead = 1;
   return false;
 }
 
@@ -264,10 +286,13 @@ __global__ void __launch_bounds__(kPfThreads, 2)
     prefix_kernel(const PfArgs a) {
   extern __shared__ uint8_t raw_smem[];
   __shared__ PfShared sh;
-  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  // the same for all of a warp, and known to be: products and copies take
+  // their operands from uniform registers
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int wid = __shfl_sync(0xffffffffu, tid >> 5, 0);
   // swizzled tiles start at multiples of 1024 bytes
   const uint32_t q_s = (smem_u32(raw_smem) + 1023u) & ~1023u;
-  const uint32_t k_s = q_s + 2 * kPfCodes;
+  const uint32_t k_s = q_s + 2 * kPfQuery;
   const uint32_t v_s = k_s + kPfCodes;
   const uint32_t raw_s = v_s + 2 * kPfBlock;  // [page][kPfRest]
 
@@ -291,10 +316,12 @@ __global__ void __launch_bounds__(kPfThreads, 2)
         : "memory");
     if (lane == 0) {
       mbar_init(&sh.k_raw, 1);
+      mbar_init(&sh.k_full, 1);
       mbar_init(&sh.v_raw, 1);
-      mbar_init(&sh.info, kPfWiden);
-      mbar_init(&sh.k_full, kPfWiden);
+      mbar_init(&sh.v_read, kPfWiden + 1);
       mbar_init(&sh.v_full, kPfWiden);
+      mbar_init(sh.info, kPfWiden + 1);
+      mbar_init(sh.info + 1, kPfWiden + 1);
       mbar_init(&sh.p_full, 4);
       mbar_init(&sh.qk_done, 1);
       mbar_init(&sh.pv_done, 1);
@@ -353,7 +380,7 @@ __global__ void __launch_bounds__(kPfThreads, 2)
       }
       const uint32_t at = q_s + tid * 128 + ((i ^ (tid & 7)) << 4);
       st_shared_v4(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-      st_shared_v4(at + kPfCodes, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+      st_shared_v4(at + kPfQuery, make_uint4(lo[0], lo[1], lo[2], lo[3]));
     }
     fence_to_async();
   }
@@ -367,16 +394,18 @@ __global__ void __launch_bounds__(kPfThreads, 2)
     const uint32_t mine = tm + ((uint32_t)(wid * 32) << 16);
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    for (int j = 0; j < n && ok; ++j) {
-      ok = pf_wait(sh, &sh.qk_done, j & 1) && pf_wait(sh, &sh.info, j & 1);
+    for (int j = 0; j < n; ++j) {
+      const int par = j & 1;
       // all products before S(j), among them O(j - 1), are done
-      if (ok && j > 0) ok = pf_wait(sh, &sh.pv_done, (j - 1) & 1);
+      ok = pf_wait(sh, sh.info + par, j >> 1 & 1) &&
+           pf_wait(sh, &sh.qk_done, j & 1) &&
+           (j == 0 || pf_wait(sh, &sh.pv_done, (j - 1) & 1));
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tm_fence_after();
-      const uint32_t there = sh.there;
-      // 64 columns: their weights go over the scores they come from, in
-      // columns that have been read
+      const uint32_t there = sh.there[par];
+      // 64 columns at a time: their weights go over the scores they come
+      // from, in columns that have been read
       for (int c = 0; c < 2; ++c) {
         uint64_t x[32];
         {
@@ -398,7 +427,7 @@ __global__ void __launch_bounds__(kPfThreads, 2)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float4 k4 =
-                reinterpret_cast<const float4 *>(sh.k_scale)[4 * pg + i];
+                reinterpret_cast<const float4 *>(sh.k_scale[par])[4 * pg + i];
             uint64_t &x0 = x[8 * p + 2 * i], &x1 = x[8 * p + 2 * i + 1];
             x0 = mul2(x0, pack2(k4.x, k4.y));
             x1 = mul2(x1, pack2(k4.z, k4.w));
@@ -406,7 +435,8 @@ __global__ void __launch_bounds__(kPfThreads, 2)
             t4[i] = fmaxf(max3(u.x, u.y, v.x), v.y);
           }
           const float t1 = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]);
-          if (there >> pg & 1) top = fmaxf(top, fmaf(t1, f, sh.v_exp[pg]));
+          if (there >> pg & 1)
+            top = fmaxf(top, fmaf(t1, f, sh.v_exp[par][pg]));
         }
         const bool raise = top > m + kPfSlack;
         if (__any_sync(0xffffffffu, raise)) {  // rare after the first tiles
@@ -441,7 +471,7 @@ __global__ void __launch_bounds__(kPfThreads, 2)
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
           const int pg = 4 * c + p;
-          const float add = sh.v_exp[pg] - (m - kPfLift);
+          const float add = sh.v_exp[par][pg] - (m - kPfLift);
           const uint64_t aa = pack2(add, add);
           uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -453,7 +483,7 @@ __global__ void __launch_bounds__(kPfThreads, 2)
           }
           if (there >> pg & 1) {
             const float2 t2 = unpack2(add2(sum[0], sum[1]));
-            l = fmaf(t2.x + t2.y, sh.v_inv[pg], l);
+            l = fmaf(t2.x + t2.y, sh.v_inv[par][pg], l);
           } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) w[8 * p + i] = 0u;
@@ -470,7 +500,7 @@ __global__ void __launch_bounds__(kPfThreads, 2)
     ok = __all_sync(0xffffffffu, ok);
     tm_fence_after();
     const size_t all = (size_t)rows * a.h_kv;
-    const size_t at = (size_t)split * all +
+    const size_t out = (size_t)split * all +
                       (size_t)(row / a.G) * a.h_kv * a.G + (size_t)h * a.G +
                       row % a.G;
     for (int c = 0; c < 4; ++c) {
@@ -479,7 +509,7 @@ __global__ void __launch_bounds__(kPfThreads, 2)
       tm_wait_ld();
       if (row < rows && ok) {
         float4 *dst =
-            reinterpret_cast<float4 *>(a.o_part + at * kDim) + 8 * c;
+            reinterpret_cast<float4 *>(a.o_part + out * kDim) + 8 * c;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           dst[i] = make_float4(
@@ -487,171 +517,211 @@ __global__ void __launch_bounds__(kPfThreads, 2)
               __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
       }
     }
-    if (row < rows) a.ml_part[at] = make_float2(m, ok ? l : 0.f);
+    if (row < rows) a.ml_part[out] = make_float2(m, ok ? l : 0.f);
   } else {
     auto good = [&](int ph) -> bool { return ph >= 0 && ph < a.num_phys; };
     // page lane & 7 of tile t as the table has it, -1 past the end
     auto page = [&](int t) -> int {
-      const int pg = t * kPfPages + (lane & 7);
+      const int pg = t * kPfPages + (lane & (kPfPages - 1));
       return t < t1 && pg < a.pages ? __ldg(a.table + pg) : -1;
     };
     auto pages_there = [&](int ph) -> uint32_t {
-      return __ballot_sync(0xffffffffu, good(ph)) & 0xffu;
+      return __ballot_sync(0xffffffffu, good(ph)) & ((1u << kPfPages) - 1);
     };
+    // keys, or values and scales, of a tile's pages (ph: page lane & 7)
+    auto copy = [&](int ph, int off, uint32_t bytes, uint32_t to,
+                    uint64_t *bar) {
+      const uint32_t there = pages_there(ph);
+      if (lane == 0) mbar_arrive_tx(bar, __popc(there) * bytes);
+      __syncwarp();
+      if (lane < kPfPages && (there >> lane & 1))
+        bulk_rows(to + lane * bytes,
+                  a.records + ((size_t)ph * a.h_kv + h) * kQRec + off, bytes,
+                  bar);
+      __syncwarp();
+      return there;
+    };
+    // pages of tiles j, j + 1
     int ph = page(t0), ph_next = page(t0 + 1);
     bool ok = true;
     if (wid == 4) {
-      // ---------------------------------------------- copies and products
-      auto copy = [&](int ph, int off, uint32_t bytes, uint32_t to,
-                      uint64_t *bar) {
-        const uint32_t there = pages_there(ph);
-        if (lane == 0) mbar_arrive_tx(bar, __popc(there) * bytes);
+      // ------------------------------------------------ products, values
+      int copied = 0;  // tiles
+      auto copy_values = [&](int ph) {
+        ++copied;
+        // a page that is not there reads as zeros (written before the
+        // arrival that the readers wait for)
+        for (uint32_t gone = ~pages_there(ph) & ((1u << kPfPages) - 1); gone;
+             gone &= gone - 1)
+          for (int i = lane; i < kPfRest / 16; i += 32)
+            st_shared_v4(raw_s + (__ffs(gone) - 1) * kPfRest + 16 * i,
+                         make_uint4(0u, 0u, 0u, 0u));
         __syncwarp();
-        if (lane < kPfPages && (there >> lane & 1))
-          bulk_rows(to + lane * bytes,
-                    a.records + ((size_t)ph * a.h_kv + h) * kQRec + off,
-                    bytes, bar);
+        copy(ph, kQOffV, kPfRest, raw_s, &sh.v_raw);
       };
-      copy(ph, 0, kQCodes, k_s, &sh.k_raw);
-      copy(ph, kQOffV, kPfRest, raw_s, &sh.v_raw);
+      const uint64_t dq = mat_desc(q_s, 16), dk = mat_desc(k_s, 16);
+      const uint64_t dv = mat_desc(v_s, kPfBlock);
+      copy_values(ph);
       for (int j = 0; j < n; ++j) {
-        if (lane < kPfPages && !good(ph) &&
-            (t0 + j) * kPfPages + lane < a.pages)
-          set_status(a.status, LOCKS_DEV_BAD_PAGE_ID);
         ok = pf_wait(sh, &sh.k_full, j & 1);
         if (!__all_sync(0xffffffffu, ok)) break;
-        if (lane == 0) {
-          tm_fence_after();
+        tm_fence_after();
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)  // hi, then lo
-            mma_ss(tm,
-                   mat_desc(q_s + (kk >> 2) * kPfCodes + (kk & 3) * 32, 16),
-                   mat_desc(k_s + (kk & 3) * 32, 16), kPfDescS, kk > 0);
+            mma_ss(tm, dq + ((kk >> 2) * (kPfQuery >> 4) + (kk & 3) * 2),
+                   dk + (kk & 3) * 2, kPfDescS, kk > 0);
           mma_commit(&sh.qk_done);
         }
         __syncwarp();
-        if (j + 1 < n) {  // S(j) done: its keys may go; values likewise
-          ok = pf_wait(sh, &sh.qk_done, j & 1);
+        if (j + 1 < n) {
+          ok = pf_wait(sh, &sh.v_read, j & 1);
           if (!__all_sync(0xffffffffu, ok)) break;
-          copy(ph_next, 0, kQCodes, k_s, &sh.k_raw);
+          copy_values(ph_next);
+          ph_next = page(t0 + j + 2);
         }
-        ok = pf_wait(sh, &sh.v_full, j & 1);
+        ok = pf_wait(sh, &sh.v_full, j & 1) && pf_wait(sh, &sh.p_full, j & 1);
         if (!__all_sync(0xffffffffu, ok)) break;
-        if (j + 1 < n) copy(ph_next, kQOffV, kPfRest, raw_s, &sh.v_raw);
-        ph = ph_next;
-        ph_next = page(t0 + j + 2);
-        ok = pf_wait(sh, &sh.p_full, j & 1);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        if (lane == 0) {
-          tm_fence_after();
+        tm_fence_after();
+        if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_ts(tm + kPfColO, tm + 8 * kk,
-                   mat_desc(v_s + kk * kPage * 128, kPfBlock), kPfDescO,
-                   j > 0 || kk > 0);
+          for (int kk = 0; kk < kPfTile / 16; ++kk)
+            mma_ts(tm + kPfColO, tm + 8 * kk, dv + kk * (kPage * 128 >> 4),
+                   kPfDescO, j > 0 || kk > 0);
           mma_commit(&sh.pv_done);
         }
         __syncwarp();
       }
-      if (lane == 0 && *(volatile int *)&sh.dead) {
+      if (*(volatile int *)&sh.dead && elect_one()) {
         // give what is in flight a last, bounded chance to finish
         set_status(a.status, LOCKS_DEV_TIMEOUT);
         mma_commit(&sh.drain);
-        mbar_wait(&sh.drain, 0, 1u << 16);
-        for (uint32_t k = 0; k < 2; ++k) {
-          mbar_wait(&sh.k_raw, k, 1u << 16);
-          mbar_wait(&sh.v_raw, k, 1u << 16);
-        }
+        q_wait(&sh.drain, 0);
+        q_wait(&sh.v_raw, (copied - 1) & 1);
       }
-    } else {
-      // --------------------------------------------------- keys and values
-      // Warp w takes pages w, w + 3, w + 6 of a tile.  Eight lanes that
-      // read and store a 16-byte group each have the same half of the dims
-      // of slots s and s + 1, which either swizzle keeps in different banks.
-      const int warp = wid - 5;
-      const int s4 = (lane >> 4) * 2 + (lane >> 2 & 1);
-      const int c = (lane & 3) | (lane >> 1 & 4);
+    } else if (wid == 5) {
+      // ------------------------------------------------------------ keys
+      int copied = 0;  // tiles
+      auto copy_keys = [&](int j, int ph) {
+        ++copied;
+        if (lane < kPfPages && !good(ph) &&
+            (t0 + j) * kPfPages + lane < a.pages)
+          set_status(a.status, LOCKS_DEV_BAD_PAGE_ID);
+        copy(ph, 0, kQCodes, k_s, &sh.k_raw);
+      };
       // the halves of odd key rows trade places
       auto mend_keys = [&]() {
-        uint4 x[3], y[3];
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          const int pair = 32 * (3 * i + warp) + lane;  // of 256
-          const uint32_t at =
-              k_s + (2 * (pair >> 2) + 1) * 128 + 16 * (pair & 3);
-          if (pair < 256) {
-            x[i] = lds128(at);
-            y[i] = lds128(at + 64);
+        for (int h2 = 0; h2 < 2; ++h2) {
+          const uint32_t at = k_s + h2 * 4 * kQCodes +
+                              (2 * (lane >> 2) + 1) * 128 + 16 * (lane & 3);
+          uint4 x[4], y[4];
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            x[p] = lds128(at + p * kQCodes);
+            y[p] = lds128(at + p * kQCodes + 64);
           }
-        }
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          const int pair = 32 * (3 * i + warp) + lane;
-          const uint32_t at =
-              k_s + (2 * (pair >> 2) + 1) * 128 + 16 * (pair & 3);
-          if (pair < 256) {
-            st_shared_v4(at, y[i]);
-            st_shared_v4(at + 64, x[i]);
+          for (int p = 0; p < 4; ++p) {
+            st_shared_v4(at + p * kQCodes, y[p]);
+            st_shared_v4(at + p * kQCodes + 64, x[p]);
           }
         }
         fence_to_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.k_full);
       };
-      // Scales of this warp's pages: what softmax needs of them, and the
-      // factors 2^(e - E) of their value rows, exact down to 2^-24 and zero
-      // below.  Lane 16 i + slot: its i-th page, and its third in lanes 0-15.
-      __half2 factor[2];
-      auto tell = [&](uint32_t there) {
+      copy_keys(0, ph);
+      ok = pf_wait(sh, &sh.k_raw, 0);
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) mend_keys();
+      for (int j = 0; j < n && ok; ++j) {
+        // what softmax needs to know of tile j (S(j - 1) is
+        // done, so O(j - 2) is, and the softmax that knew of j - 2)
+        ok = pf_wait(sh, &sh.v_raw, j & 1);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        const uint32_t there = pages_there(ph);
+#pragma unroll
+        for (int i = 0; i < kPfPages / 2; ++i) {
+          const int pg = 2 * i + (lane >> 4), sl = lane & 15;
+          uint32_t e;
+          asm volatile("ld.shared.u8 %0, [%1];\n"
+                       : "=r"(e)
+                       : "r"(raw_s + pg * kPfRest + (kQOffKE - kQOffV) + sl));
+          sh.k_scale[j & 1][kPage * pg + sl] = __uint_as_float(e << 23);
+        }
+        if (lane == 0) sh.there[j & 1] = there;
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(sh.info + (j & 1));
+          mbar_arrive(&sh.v_read);
+        }
+        ph = ph_next;
+        if (j + 1 < n) {  // S(j) done: its keys may go
+          ok = pf_wait(sh, &sh.qk_done, j & 1);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          copy_keys(j + 1, ph);
+          ph_next = page(t0 + j + 2);
+          ok = pf_wait(sh, &sh.k_raw, (j + 1) & 1);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          mend_keys();
+        }
+      }
+      if (*(volatile int *)&sh.dead) q_wait(&sh.k_raw, (copied - 1) & 1);
+    } else {
+      // ---------------------------------------------------------- values
+      // A warp takes four pages of a tile, four slots at a time.  Eight
+      // lanes that read and store a 16-byte group each have the same half of
+      // the dims of slots s and s + 1, which either swizzle keeps in
+      // different banks.
+      const int first = 4 * (wid - 6);
+      const int s4 = (lane >> 4) * 2 + (lane >> 2 & 1);
+      const int c = (lane & 3) | (lane >> 1 & 4);
+      for (int j = 0; j < n; ++j) {
+        ok = pf_wait(sh, &sh.v_raw, j & 1);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        uint4 raw[16];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+          const int sl = 4 * (u & 3) + s4;
+          raw[u] = lds128(raw_s + (first + (u >> 2)) * kPfRest + sl * kDim +
+                          16 * q_group(c, sl));
+        }
+        // lane 16 i + slot: scales of rows of pages i and 2 + i; factor:
+        // 2^(e - E), exact down to 2^-24 and zero below
+        uint32_t factor[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int pg = warp + 6 * i + 3 * (lane >> 4), sl = lane & 15;
-          const bool in = pg < kPfPages && (there >> pg & 1);
-          uint32_t ek = 127, ev = 127;
-          if (in) {
-            const uint32_t at =
-                raw_s + pg * kPfRest + (kQOffKE - kQOffV) + sl;
-            asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(ek) : "r"(at));
-            asm volatile("ld.shared.u8 %0, [%1];\n"
-                         : "=r"(ev)
-                         : "r"(at + kPage));
-          }
-          uint32_t top = ev;
+          const int pg = first + 2 * i + (lane >> 4);
+          uint32_t e;
+          asm volatile("ld.shared.u8 %0, [%1];\n"
+                       : "=r"(e)
+                       : "r"(raw_s + pg * kPfRest + (kQOffVE - kQOffV) +
+                             (lane & 15)));
+          uint32_t top = e;
 #pragma unroll
           for (int o = 1; o < 16; o <<= 1)
             top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-          if (pg < kPfPages) {
-            sh.k_scale[kPage * pg + sl] = __uint_as_float(ek << 23);
-            if (sl == 0) {
-              sh.v_exp[pg] = (float)((int)top - 127);
-              sh.v_inv[pg] = exp2_int(127 - (int)top);
-            }
+          if ((lane & 15) == 0) {
+            sh.v_exp[j & 1][pg] = (float)((int)top - 127);
+            sh.v_inv[j & 1][pg] = exp2_int(127 - (int)top);
           }
-          factor[i] =
-              __float2half2_rn(exp2_int(max(-126, (int)ev - (int)top)));
+          factor[i] = h2_as_u32(
+              __float2half2_rn(exp2_int(max(-126, (int)e - (int)top))));
         }
-        if (warp == 0 && lane == 0) sh.there = there;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.info);
-      };
-      auto store_values = [&](uint32_t there) {
-        // all loads first, then page by page
-        uint4 raw[12];
-#pragma unroll
-        for (int u = 0; u < 12; ++u) {  // page u / 4, its slots 4 (u % 4) ..
-          const int p = warp + 3 * (u >> 2), sl = 4 * (u & 3) + s4;
-          raw[u] = p < kPfPages && (there >> p & 1)
-                       ? lds128(raw_s + p * kPfRest + sl * kDim +
-                                16 * q_group(c, sl))
-                       : make_uint4(0u, 0u, 0u, 0u);
+        if (lane == 0) {
+          mbar_arrive(sh.info + (j & 1));
+          mbar_arrive(&sh.v_read);
         }
+        // O(j - 1) done: its values may go
+        ok = j == 0 || pf_wait(sh, &sh.pv_done, (j - 1) & 1);
+        if (!__all_sync(0xffffffffu, ok)) break;
 #pragma unroll
-        for (int u = 0; u < 12; ++u) {
-          const int p = warp + 3 * (u >> 2), sl = 4 * (u & 3) + s4;
-          const __half2 x = u32_as_h2(
-              __shfl_sync(0xffffffffu, h2_as_u32(factor[u >> 3]),
-                          16 * (u >> 2 & 1) + sl));
-          if (p >= kPfPages) break;
+        for (int u = 0; u < 16; ++u) {
+          const int sl = 4 * (u & 3) + s4;
+          const __half2 x = u32_as_h2(__shfl_sync(
+              0xffffffffu, factor[u >> 3], 16 * (u >> 2 & 1) + sl));
           const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
           uint32_t y[8];
 #pragma unroll
@@ -659,7 +729,7 @@ __global__ void __launch_bounds__(kPfThreads, 2)
             y[2 * k] = h2_as_u32(__hmul2(u32_as_h2(e4m3x2_lo(w[k])), x));
             y[2 * k + 1] = h2_as_u32(__hmul2(u32_as_h2(e4m3x2_hi(w[k])), x));
           }
-          const int r = p * kPage + sl;
+          const int r = (first + (u >> 2)) * kPage + sl;
           st_shared_v4(v_s + tile_at(r, 2 * c),
                        make_uint4(y[0], y[1], y[2], y[3]));
           st_shared_v4(v_s + tile_at(r, 2 * c + 1),
@@ -668,20 +738,6 @@ __global__ void __launch_bounds__(kPfThreads, 2)
         fence_to_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.v_full);
-      };
-      for (int j = 0; j < n; ++j) {
-        ok = pf_wait(sh, &sh.k_raw, j & 1);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        mend_keys();
-        const uint32_t there = pages_there(ph);
-        ph = ph_next;
-        ph_next = page(t0 + j + 2);
-        // O(j - 1) done: its values, and what softmax knew, may go
-        ok = (j == 0 || pf_wait(sh, &sh.pv_done, (j - 1) & 1)) &&
-             pf_wait(sh, &sh.v_raw, j & 1);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        tell(there);
-        store_values(there);
       }
     }
   }

@@ -359,14 +359,15 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
   };
 
   uint32_t phase = 0;
-  for (int st = 0; fn[0] > 0;) {
+  int st = 0;
+  while (fn[0] > 0) {
     const int ntok = fn[0];
     if (!UNIT && fu[0] != cur) advance(fu[0]);
     if (!q_ready) {
       load_q(cur);
       q_ready = true;
     }
-    if (!mbar_wait(bar + st, phase)) {
+    if (!q_wait(bar + st, phase)) {
       dead = true;
       break;
     }
@@ -516,10 +517,11 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
   }
   if (dead) {  // give the copies in flight a last, bounded chance to land
     if (lane == 0) set_status(a.status, LOCKS_DEV_TIMEOUT);
-    for (int i = 0; i < kQdStages; ++i) {
-      mbar_wait(bar + i, 0, 1u << 16);
-      mbar_wait(bar + i, 1, 1u << 16);
-    }
+    for (int i = 0; i < kQdStages; ++i)
+      if (fn[i] > 0) {
+        const int at = st + i < kQdStages ? st + i : st + i - kQdStages;
+        q_wait(bar + at, phase ^ (st + i < kQdStages ? 0u : 1u));
+      }
   }
   __syncwarp();
 

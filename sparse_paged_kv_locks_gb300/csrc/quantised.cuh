@@ -73,6 +73,20 @@ __device__ __forceinline__ uint32_t e4m3x2_hi(uint32_t x) {
   return r;
 }
 
+// Waits are bounded in time (about a second), not in tries: a try may itself
+// wait on the barrier for as long as the hardware likes.
+constexpr long long kQWaitCycles = 1LL << 31;
+
+// false when the barrier did not complete in time
+__device__ __forceinline__ bool q_wait(uint64_t *bar, uint32_t phase) {
+  if (mbar_try_wait(bar, phase)) return true;
+  const long long t0 = clock64();
+  do {
+    if (mbar_try_wait(bar, phase)) return true;
+  } while (clock64() - t0 < kQWaitCycles);
+  return false;
+}
+
 // ---------------------------------------------------------------------------
 // page lists
 // ---------------------------------------------------------------------------
