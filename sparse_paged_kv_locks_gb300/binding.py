@@ -463,42 +463,66 @@ def new_prefix_workspace(batch, h_q, h_kv, max_pages, prefix_pages,
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
-def _req_rows(t, name):
-    """[n][h_kv][128] rows of any token and head stride, dims contiguous."""
+def _addr(t):
+    """Device address, as the number that ctypes passes for a pointer."""
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream):
+    return (torch.cuda.current_stream() if stream is None
+            else stream).cuda_stream
+
+
+def _req_on(index, t, name, dtype, ndim=None):
+    """_req, and on GPU `index` (of the cache)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on the cache's GPU")
+    if ndim is not None and t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dims, got {t.dim()}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _req_records(cache):
+    _req(cache, "cache", torch.uint8, 3)
+    P, h_kv, n = cache.shape
+    if n != KV_RECORD_BYTES:
+        raise ValueError("cache must be [num_phys_pages][h_kv][4128]")
+    return P, h_kv, cache.get_device()
+
+
+def _req_rows(index, t, name):
+    """[n][h_kv][128] rows of any token and head stride, dims contiguous;
+    the two strides (that of a dimension of one entry says nothing)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in _TYPES:
         raise TypeError(f"{name} must be bfloat16, float16 or float32, got "
                         f"{t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on the cache's GPU")
     if t.dim() != 3 or t.shape[2] != HEAD_DIM or t.stride(2) != 1:
         raise ValueError(f"{name} must be [n][h_kv][128] with contiguous "
                          "rows")
-    step = 16 // t.element_size()
-    if t.data_ptr() % 16 or any(t.shape[i] > 1 and t.stride(i) % step
-                                for i in (0, 1)):
+    n, h, _ = t.shape
+    a, b, _ = t.stride()
+    a, b = a if n > 1 else 0, b if h > 1 else 0
+    if (t.data_ptr() | a * t.element_size() | b * t.element_size()) % 16:
         raise ValueError(f"{name}'s rows must start at multiples of 16 bytes")
+    return a, b
 
 
-def _req_records(cache):
-    _req(cache, "cache", torch.uint8, 3)
-    if cache.shape[2] != KV_RECORD_BYTES:
-        raise ValueError("cache must be [num_phys_pages][h_kv][4128]")
-    return cache.shape[:2]
-
-
-def _req_pairs(a, b, names):
-    for t, name in zip((a, b), names):
-        _req(t, name, torch.int32, 1)
-    if a.numel() != b.numel():
+def _req_pairs(index, a, b, names):
+    _req_on(index, a, names[0], torch.int32, 1)
+    _req_on(index, b, names[1], torch.int32, 1)
+    n = a.numel()
+    if b.numel() != n:
         raise ValueError(f"{names[0]} and {names[1]} differ in length")
-
-
-def _req_same_device(cache, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != cache.device:
-            raise ValueError(f"{name} and cache are on different devices")
+    return n
 
 
 def locks_quantise_kv(k_new, v_new, seq_ids, positions, page_table, cache,
@@ -506,28 +530,23 @@ def locks_quantise_kv(k_new, v_new, seq_ids, positions, page_table, cache,
     """Rows k_new, v_new [n][h_kv][128] (bfloat16, float16 or float32; token
     and head strides free) into position positions[i] of sequence
     seq_ids[i] (seq_id < 0: skipped)."""
-    P, h_kv = _req_records(cache)
-    _req_rows(k_new, "k_new")
-    _req_rows(v_new, "v_new")
-    _req_pairs(seq_ids, positions, ("seq_ids", "positions"))
-    _req(page_table, "page_table", torch.int32, 2)
-    n = seq_ids.numel()
-    if tuple(k_new.shape) != (n, h_kv, HEAD_DIM) or \
-            k_new.shape != v_new.shape or k_new.dtype != v_new.dtype:
+    P, h_kv, index = _req_records(cache)
+    ks, vs = _req_rows(index, k_new, "k_new"), _req_rows(index, v_new, "v_new")
+    n = _req_pairs(index, seq_ids, positions, ("seq_ids", "positions"))
+    _req_on(index, page_table, "page_table", torch.int32, 2)
+    if k_new.shape != (n, h_kv, HEAD_DIM) or k_new.shape != v_new.shape or \
+            k_new.dtype is not v_new.dtype:
         raise ValueError("k_new and v_new must be [n][h_kv][128] of one type")
     if status is not None:
-        _req(status, "status", torch.int32)
-    _req_same_device(cache, k_new=k_new, v_new=v_new, seq_ids=seq_ids,
-                     positions=positions, page_table=page_table,
-                     status=status)
+        _req_on(index, status, "status", torch.int32)
     batch, max_pages = page_table.shape
-    # the stride of a dimension of one entry says nothing
-    ks, vs = ([t.stride(i) if t.shape[i] > 1 else 0 for i in (0, 1)]
-              for t in (k_new, v_new))
-    _check("locks_quantise_kv", lib().locks_quantise_kv(
-        _ptr(k_new), _ptr(v_new), _TYPES[k_new.dtype], *ks, *vs,
-        _ptr(seq_ids), _ptr(positions), n, _ptr(cache), P, h_kv,
-        _ptr(page_table), batch, max_pages, _ptr(status), _stream(stream)))
+    rc = lib().locks_quantise_kv(
+        k_new.data_ptr(), v_new.data_ptr(), _TYPES[k_new.dtype], *ks, *vs,
+        seq_ids.data_ptr(), positions.data_ptr(), n, cache.data_ptr(), P,
+        h_kv, page_table.data_ptr(), batch, max_pages, _addr(status),
+        _raw_stream(stream))
+    if rc:
+        _check("locks_quantise_kv", rc)
 
 
 def locks_dequantise_kv(cache, page_table, seq_ids, page_ids, k_out, v_out,
@@ -535,76 +554,74 @@ def locks_dequantise_kv(cache, page_table, seq_ids, page_ids, k_out, v_out,
     """Pages (seq_ids[i], page_ids[i]) back as numbers in k_out, v_out
     [n][h_kv][16][128] (bfloat16, float16 or float32; either may be None);
     with seq_lens, slots past a sequence's end read as zeros."""
-    P, h_kv = _req_records(cache)
-    _req_pairs(seq_ids, page_ids, ("seq_ids", "page_ids"))
-    _req(page_table, "page_table", torch.int32, 2)
-    n = seq_ids.numel()
-    outs = [t for t in (k_out, v_out) if t is not None]
-    if not outs:
+    P, h_kv, index = _req_records(cache)
+    n = _req_pairs(index, seq_ids, page_ids, ("seq_ids", "page_ids"))
+    _req_on(index, page_table, "page_table", torch.int32, 2)
+    one = k_out if k_out is not None else v_out
+    if one is None:
         raise ValueError("k_out or v_out must be given")
+    if not isinstance(one, torch.Tensor) or one.dtype not in _TYPES:
+        raise TypeError("k_out and v_out must be bfloat16, float16 or float32 "
+                        "tensors")
     for t, name in ((k_out, "k_out"), (v_out, "v_out")):
         if t is None:
             continue
-        if not isinstance(t, torch.Tensor) or t.dtype not in _TYPES:
-            raise TypeError(f"{name} must be a bfloat16, float16 or float32 "
-                            "tensor")
-        _req(t, name, outs[0].dtype, 4)
-        if tuple(t.shape) != (n, h_kv, PAGE, HEAD_DIM):
+        _req_on(index, t, name, one.dtype, 4)
+        if t.shape != (n, h_kv, PAGE, HEAD_DIM):
             raise ValueError(f"{name} must be [n][h_kv][16][128]")
     batch, max_pages = page_table.shape
     if seq_lens is not None:
-        _req(seq_lens, "seq_lens", torch.int32, 1)
+        _req_on(index, seq_lens, "seq_lens", torch.int32, 1)
         if seq_lens.numel() != batch:
             raise ValueError("seq_lens must have one entry per sequence")
     if status is not None:
-        _req(status, "status", torch.int32)
-    _req_same_device(cache, page_table=page_table, seq_ids=seq_ids,
-                     page_ids=page_ids, k_out=k_out, v_out=v_out,
-                     seq_lens=seq_lens, status=status)
-    _check("locks_dequantise_kv", lib().locks_dequantise_kv(
-        _ptr(cache), P, h_kv, _ptr(page_table), batch, max_pages,
-        _ptr(seq_ids), _ptr(page_ids), n, _ptr(seq_lens),
-        _TYPES[outs[0].dtype], _ptr(k_out), _ptr(v_out), _ptr(status),
-        _stream(stream)))
+        _req_on(index, status, "status", torch.int32)
+    rc = lib().locks_dequantise_kv(
+        cache.data_ptr(), P, h_kv, page_table.data_ptr(), batch, max_pages,
+        seq_ids.data_ptr(), page_ids.data_ptr(), n, _addr(seq_lens),
+        _TYPES[one.dtype], _addr(k_out), _addr(v_out), _addr(status),
+        _raw_stream(stream))
+    if rc:
+        _check("locks_dequantise_kv", rc)
 
 
-def _req_decode(q, cache, page_table, seq_lens, o_out, lse_out, workspace,
-                **more):
-    P, h_kv = _req_records(cache)
-    _req(q, "q", torch.bfloat16, 3)
-    _req(page_table, "page_table", torch.int32, 2)
-    _req(seq_lens, "seq_lens", torch.int32, 1)
-    _req(o_out, "o_out", torch.bfloat16, 3)
-    _req(lse_out, "lse_out", torch.float32, 2)
-    _req(workspace, "workspace", torch.uint8, 1)
+def _req_decode(q, cache, page_table, seq_lens, o_out, lse_out, workspace):
+    P, h_kv, index = _req_records(cache)
+    _req_on(index, q, "q", torch.bfloat16, 3)
+    _req_on(index, page_table, "page_table", torch.int32, 2)
+    _req_on(index, seq_lens, "seq_lens", torch.int32, 1)
+    _req_on(index, o_out, "o_out", torch.bfloat16, 3)
+    _req_on(index, lse_out, "lse_out", torch.float32, 2)
+    _req_on(index, workspace, "workspace", torch.uint8, 1)
     batch, h_q, d = q.shape
     if d != HEAD_DIM or o_out.shape != q.shape or \
-            tuple(lse_out.shape) != (batch, h_q):
+            lse_out.shape != (batch, h_q):
         raise ValueError("q and o_out must be [batch][h_q][128], lse_out "
                          "[batch][h_q]")
-    if page_table.shape[0] != batch or seq_lens.numel() != batch:
+    rows, max_pages = page_table.shape
+    if rows != batch or seq_lens.numel() != batch:
         raise ValueError("page_table and seq_lens must have one entry per "
                          "sequence")
-    _req_same_device(cache, q=q, page_table=page_table, seq_lens=seq_lens,
-                     o_out=o_out, lse_out=lse_out, workspace=workspace,
-                     **more)
-    return P, h_kv, batch, h_q, page_table.shape[1]
+    return P, h_kv, batch, h_q, max_pages, index
 
 
 def locks_quantised_decode(q, cache, page_table, seq_lens, idx, k, o_out,
                            lse_out, workspace, stream=None):
     """locks_sparse_decode over the quantised cache (idx None: every
     page)."""
-    P, h_kv, batch, h_q, max_pages = _req_decode(
-        q, cache, page_table, seq_lens, o_out, lse_out, workspace, idx=idx)
+    P, h_kv, batch, h_q, max_pages, index = _req_decode(
+        q, cache, page_table, seq_lens, o_out, lse_out, workspace)
     if idx is not None:
-        _req(idx, "idx", torch.int32, 3)
-        if tuple(idx.shape) != (batch, h_kv, k):
+        _req_on(index, idx, "idx", torch.int32, 3)
+        if idx.shape != (batch, h_kv, k):
             raise ValueError("idx must be [batch][h_kv][k]")
-    _check("locks_quantised_decode", lib().locks_quantised_decode(
-        _ptr(q), _ptr(cache), P, _ptr(page_table), _ptr(seq_lens), _ptr(idx),
-        k, batch, h_q, h_kv, max_pages, _ptr(o_out), _ptr(lse_out),
-        _ptr(workspace), workspace.numel(), _stream(stream)))
+    rc = lib().locks_quantised_decode(
+        q.data_ptr(), cache.data_ptr(), P, page_table.data_ptr(),
+        seq_lens.data_ptr(), _addr(idx), k, batch, h_q, h_kv, max_pages,
+        o_out.data_ptr(), lse_out.data_ptr(), workspace.data_ptr(),
+        workspace.numel(), _raw_stream(stream))
+    if rc:
+        _check("locks_quantised_decode", rc)
 
 
 def locks_prefix_decode(q, cache, prefix_table, page_table, seq_lens, o_out,
@@ -612,15 +629,16 @@ def locks_prefix_decode(q, cache, prefix_table, page_table, seq_lens, o_out,
     """Attention over every page, where all sequences begin with the pages
     prefix_table [prefix_pages] (their tables' first entries are not
     read)."""
-    _req(prefix_table, "prefix_table", torch.int32, 1)
-    P, h_kv, batch, h_q, max_pages = _req_decode(
-        q, cache, page_table, seq_lens, o_out, lse_out, workspace,
-        prefix_table=prefix_table)
-    _check("locks_prefix_decode", lib().locks_prefix_decode(
-        _ptr(q), _ptr(cache), P, _ptr(prefix_table), prefix_table.numel(),
-        _ptr(page_table), _ptr(seq_lens), batch, h_q, h_kv, max_pages,
-        _ptr(o_out), _ptr(lse_out), _ptr(workspace), workspace.numel(),
-        _stream(stream)))
+    P, h_kv, batch, h_q, max_pages, index = _req_decode(
+        q, cache, page_table, seq_lens, o_out, lse_out, workspace)
+    _req_on(index, prefix_table, "prefix_table", torch.int32, 1)
+    rc = lib().locks_prefix_decode(
+        q.data_ptr(), cache.data_ptr(), P, prefix_table.data_ptr(),
+        prefix_table.numel(), page_table.data_ptr(), seq_lens.data_ptr(),
+        batch, h_q, h_kv, max_pages, o_out.data_ptr(), lse_out.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), _raw_stream(stream))
+    if rc:
+        _check("locks_prefix_decode", rc)
 
 
 def locks_clear_status(status_word, stream=None):

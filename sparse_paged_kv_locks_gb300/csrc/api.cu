@@ -522,7 +522,8 @@ static locks_status_t check_qdecode(const void *q, const void *records,
   if (h_q / h_kv > kMaxGroup) return LOCKS_ERR_UNSUPPORTED;
   if (batch > qdecode_max_batch() || h_kv > 65535) return LOCKS_ERR_UNSUPPORTED;
   if ((long long)max_pages * kPage > 0x7fffffffLL ||
-      (long long)batch * h_kv * list_len > 0x7fffffffLL)
+      (long long)batch * h_kv * list_len > 0x7fffffffLL ||
+      (long long)batch * h_q > 0x7fffffffLL)
     return LOCKS_ERR_UNSUPPORTED;
   if (batch == 0) return LOCKS_OK;
   if (!q || !records || !page_table || !seq_lens || !o_out || !lse_out ||

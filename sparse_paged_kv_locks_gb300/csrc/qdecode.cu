@@ -40,7 +40,8 @@ constexpr float kQdSlack = 7.f;   // .. and m trails the maximum by at most 7
 
 // One lane's entry of a window of 32 positions.
 struct QEntry {
-  int phys, ntok, u;  // phys < 0: nothing to read
+  const uint8_t *record;  // null: nothing to read
+  int ntok, u;
 };
 
 struct QdArgs {
@@ -71,7 +72,7 @@ __device__ __forceinline__ int own_pages(const QdArgs &a, int L) {
 __device__ __forceinline__ QEntry q_resolve(const QdArgs &a,
                                             const PageLists &lists, int p,
                                             int pe) {
-  QEntry e{-1, 0, 0};
+  QEntry e{nullptr, 0, 0};
   if (p >= pe) return e;
   const int b = lists.sequence(p);
   const int len = lists.length(b);
@@ -79,12 +80,18 @@ __device__ __forceinline__ QEntry q_resolve(const QdArgs &a,
   const int h = r / len;
   int pg = r - h * len;
   e.u = b * lists.h_kv + h;
-  const int L = checked_len(a.seq_lens, b, a.max_pages, a.status);
-  const int n = (L + kPage - 1) / kPage;
   const int32_t *table = a.pt + (size_t)b * a.max_pages;
+  int ph = 0;
   if (a.idx) {
+    // the table entry is read beside the length it is checked against, where
+    // the table has one
     pg = __ldg(a.idx + (size_t)e.u * a.k + pg);
     if (pg < 0) return e;
+    ph = pg < a.max_pages ? __ldg(table + pg) : -1;
+  }
+  const int L = checked_len(a.seq_lens, b, a.max_pages, a.status);
+  const int n = (L + kPage - 1) / kPage;
+  if (a.idx) {
     if (pg >= n) {
       set_status(a.status, LOCKS_DEV_BAD_INDEX);
       return e;
@@ -95,12 +102,12 @@ __device__ __forceinline__ QEntry q_resolve(const QdArgs &a,
     else
       table = a.prefix;
   }
-  const int ph = __ldg(table + pg);
+  if (!a.idx) ph = __ldg(table + pg);
   if (ph < 0 || ph >= a.num_phys) {
     set_status(a.status, LOCKS_DEV_BAD_PAGE_ID);
     return e;
   }
-  e.phys = ph;
+  e.record = a.records + ((size_t)ph * lists.h_kv + h) * kQRec;
   e.ntok = min(kPage, L - pg * kPage);
   return e;
 }
@@ -198,42 +205,33 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
   // window of 32 positions: this lane's entry, and those not yet copied
   int win = pb - 32;
   uint32_t left = 0;
-  QEntry we{-1, 0, 0};
-  auto next = [&](int &phys, int &ntok, int &u) {
+  QEntry we{nullptr, 0, 0};
+  // has the next entry copied to stage st; its tokens (0: none left), unit
+  auto issue = [&](int st, int &ntok, int &u) {
     while (left == 0) {
       win += 32;
       if (win >= pe) {
-        phys = -1;
+        ntok = 0;
         return;
       }
       we = q_resolve(a, lists, win + lane, pe);
-      left = __ballot_sync(0xffffffffu, we.phys >= 0);
+      left = __ballot_sync(0xffffffffu, we.record != nullptr);
     }
     const int j = __ffs(left) - 1;
     left &= left - 1;
-    phys = __shfl_sync(0xffffffffu, we.phys, j);
-    ntok = __shfl_sync(0xffffffffu, we.ntok, j);
-    u = __shfl_sync(0xffffffffu, we.u, j);
-  };
-  auto issue = [&](int st, int phys, int u) {
-    if (lane == 0) {
+    if (lane == j) {
       mbar_arrive_tx(bar + st, kQRec);
-      bulk_g2s(ring + st * kQdStride,
-               a.records + ((size_t)phys * a.h_kv + u % a.h_kv) * kQRec, kQRec,
-               bar + st);
+      bulk_g2s(ring + st * kQdStride, we.record, kQRec, bar + st);
     }
+    ntok = __shfl_sync(0xffffffffu, we.ntok, j);
+    u = UNIT ? 0 : __shfl_sync(0xffffffffu, we.u, j);
   };
-  // copies in flight, oldest first (tokens 0: none)
+  // copies in flight, oldest first
   int fn[kQdStages], fu[kQdStages];
 #pragma unroll
   for (int i = 0; i < kQdStages; ++i) {
-    int phys;
     fn[i] = fu[i] = 0;
-    next(phys, fn[i], fu[i]);
-    if (phys < 0)
-      fn[i] = 0;
-    else
-      issue(i, phys, fu[i]);
+    issue(i, fn[i], fu[i]);
   }
 
   // query B fragments of a unit: column n = head 8 nt + g of the group,
@@ -358,6 +356,16 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
     }
   };
 
+  // where this lane reads in a record: key codes of tokens g, g + 8, groups
+  // t, t + 4; value codes of tokens 2t, 2t + 1, 2t + 8, 2t + 9, group g; the
+  // scales of tokens g, g + 8
+  const uint32_t k_at = ring_s + g * kDim + 16 * q_group(t, g);
+  const uint32_t k_at4 = ring_s + g * kDim + 16 * q_group(t + 4, g);
+  const uint32_t v_at = ring_s + kQOffV + 2 * t * kDim + 16 * q_group(g, 2 * t);
+  const uint32_t v_at1 =
+      ring_s + kQOffV + (2 * t + 1) * kDim + 16 * q_group(g, 2 * t + 1);
+  const uint32_t e_at = ring_s + kQOffKE + g;
+
   uint32_t phase = 0;
   int st = 0;
   while (fn[0] > 0) {
@@ -371,35 +379,32 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
       dead = true;
       break;
     }
-    const uint32_t rec = ring_s + st * kQdStride;
-
-    // key codes of tokens g, g + 8: groups t, t + 4; value codes of tokens
-    // 2t, 2t + 1, 2t + 8, 2t + 9: group g
+    const uint32_t off = st * kQdStride;
     uint4 kc[2][2], vc[4];
+    kc[0][0] = lds128(k_at + off);
+    kc[1][0] = lds128(k_at + off + 8 * kDim);
+    kc[0][1] = lds128(k_at4 + off);
+    kc[1][1] = lds128(k_at4 + off + 8 * kDim);
+    uint32_t ek[2], e2[2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        kc[r][j] = lds128(rec + (g + 8 * r) * kDim +
-                          16 * q_group(t + 4 * j, g));
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int tok = 2 * t + (r & 1) + 8 * (r >> 1);
-      vc[r] = lds128(rec + kQOffV + tok * kDim + 16 * q_group(g, tok));
+    for (int r = 0; r < 2; ++r) {
+      asm volatile("ld.shared.u8 %0, [%1];\n"
+                   : "=r"(ek[r])
+                   : "r"(e_at + off + 8 * r));
+      asm volatile("ld.shared.u8 %0, [%1];\n"
+                   : "=r"(e2[r])
+                   : "r"(e_at + off + kPage + 8 * r));
     }
+    vc[0] = lds128(v_at + off);
+    vc[1] = lds128(v_at1 + off);
+    vc[2] = lds128(v_at + off + 8 * kDim);
+    vc[3] = lds128(v_at1 + off + 8 * kDim);
     float ks[2], ev[2], vi[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      uint32_t ek, e2;
-      asm volatile("ld.shared.u8 %0, [%1];\n"
-                   : "=r"(ek)
-                   : "r"(rec + kQOffKE + g + 8 * r));
-      asm volatile("ld.shared.u8 %0, [%1];\n"
-                   : "=r"(e2)
-                   : "r"(rec + kQOffVE + g + 8 * r));
-      ks[r] = __uint_as_float(ek << 23);
-      ev[r] = (float)((int)e2 - 127);
-      vi[r] = __uint_as_float((254u - e2) << 23);
+      ks[r] = __uint_as_float(ek[r] << 23);
+      ev[r] = (float)((int)e2[r] - 127);
+      vi[r] = __uint_as_float((254u - e2[r]) << 23);
     }
     if (ntok < kPage) {  // rows past the end hold anything
 #pragma unroll
@@ -409,10 +414,11 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
     }
 
     // scores: rows = tokens, columns = heads
-    float s[NT][4];
+    float s[NT][4], s2[NT][4];  // two chains of four products
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
-      s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[nt][i] = s2[nt][i] = 0.f;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const uint32_t k0[4] = {kc[0][j].x, kc[0][j].y, kc[0][j].z, kc[0][j].w};
@@ -423,9 +429,14 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
                                 e4m3x2_hi(k0[w]), e4m3x2_hi(k1[w])};
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-          mma_f16(s[nt], fa, qb[nt][4 * j + w][0], qb[nt][4 * j + w][1]);
+          mma_f16(w & 1 ? s2[nt] : s[nt], fa, qb[nt][4 * j + w][0],
+                  qb[nt][4 * j + w][1]);
       }
     }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[nt][i] += s2[nt][i];
 
     // weights
     const bool in0 = g < ntok, in1 = g + 8 < ntok;
@@ -503,13 +514,7 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
       fn[i] = fn[i + 1];
       fu[i] = fu[i + 1];
     }
-    int phys;
-    fn[kQdStages - 1] = fu[kQdStages - 1] = 0;
-    next(phys, fn[kQdStages - 1], fu[kQdStages - 1]);
-    if (phys < 0)
-      fn[kQdStages - 1] = 0;
-    else
-      issue(st, phys, fu[kQdStages - 1]);
+    issue(st, fn[kQdStages - 1], fu[kQdStages - 1]);
     if (++st == kQdStages) {
       st = 0;
       phase ^= 1;
@@ -600,24 +605,24 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
 // ---------------------------------------------------------------------------
 // merge of partials
 // ---------------------------------------------------------------------------
-// One warp per (sequence, query head) row, four dims to a lane: the pieces
-// that the runs left of the row's unit, and before them the partials of the
-// shared prefix where there is one (`shared` of them, [split][batch * h_q],
-// skipped by sequences shorter than the prefix).  Eight partials' loads are
-// in flight at a time.
+// A CTA per (sequence, query head) row, its warps every fourth partial, four
+// dims to a lane: the pieces that the runs left of the row's unit, and before
+// them the partials of the shared prefix where there is one (`shared` of them,
+// [split][batch * h_q], skipped by sequences shorter than the prefix).  The
+// references come first, all at once (a thread each), so that the sums' loads
+// depend on nothing and are in flight together.
 constexpr int kMergeWarps = 4;
-constexpr int kMergeGroup = 8;
+constexpr int kMergeMax = 32 * kMergeWarps;  // partials weighed at a time
 
 __global__ void __launch_bounds__(32 * kMergeWarps)
     merge_kernel(const QdArgs a, const float *__restrict__ shared_o,
                  const float2 *__restrict__ shared_ml, int shared) {
+  __shared__ float s_weight[kMergeMax], s_red[2][kMergeWarps];
+  __shared__ float4 s_acc[kMergeWarps][32];
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const long long rows = (long long)a.batch * a.h_kv * a.G;
-  const long long row =
-      (long long)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
-  if (row >= rows) return;
-  const int u = (int)(row / a.G), hd = (int)(row - (long long)u * a.G);
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int rows = a.batch * a.h_kv * a.G, row = blockIdx.x;
+  const int u = row / a.G, hd = row - u * a.G;
   const int b = u / a.h_kv;
   const PageLists lists{a.meta + 1, a.batch, a.h_kv,
                         a.idx ? a.h_kv * a.k : 0};
@@ -634,48 +639,73 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
     if (L < a.prefix_pages * kPage) shared = 0;
   }
   const int n = shared + own;
-  float M = -INFINITY, sum = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 < n; s0 += kMergeGroup) {
-    float2 ml[kMergeGroup];
-    float4 v[kMergeGroup];
+  auto place = [&](int s) -> size_t {
+    return s < shared ? (size_t)s * rows + row
+                      : ((size_t)u + w0 + (s - shared)) * a.G + hd;
+  };
+  float M = -INFINITY, sum = 0.f;  // the same in all threads
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);  // this warp's share
+  for (int s0 = 0; s0 < n; s0 += kMergeMax) {
+    const int s = s0 + threadIdx.x;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (s < n) ml = (s < shared ? shared_ml : a.ml_part)[place(s)];
+    float top = ml.x;
 #pragma unroll
-    for (int i = 0; i < kMergeGroup; ++i) {
-      const int s = s0 + i;
-      ml[i] = make_float2(-INFINITY, 0.f);
-      v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (s >= n) continue;
-      const size_t at = s < shared
-                            ? (size_t)s * rows + row
-                            : ((size_t)u + w0 + (s - shared)) * a.G + hd;
-      ml[i] = (s < shared ? shared_ml : a.ml_part)[at];
-      v[i] = reinterpret_cast<const float4 *>(s < shared ? shared_o
-                                                         : a.o_part)
-                 [at * (kDim / 4) + lane];
-    }
-    float top = M;
+    for (int o = 1; o < 32; o <<= 1)
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) s_red[0][wid] = top;
+    __syncthreads();
+    top = M;
 #pragma unroll
-    for (int i = 0; i < kMergeGroup; ++i) top = fmaxf(top, ml[i].x);
+    for (int w = 0; w < kMergeWarps; ++w) top = fmaxf(top, s_red[0][w]);
     const float fall = M == top ? 1.f : ex2_fast(M - top);
     M = top;
+    // nothing from a partial without tokens; one whose scores are not
+    // numbers carries that on
+    const float x = ml.y == 0.f ? 0.f : ml.x == M ? 1.f : ex2_fast(ml.x - M);
+    float part = x * ml.y;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+      part += __shfl_xor_sync(0xffffffffu, part, o);
+    if (lane == 0) s_red[1][wid] = part;
+    s_weight[threadIdx.x] = x;
+    __syncthreads();
     sum *= fall;
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) sum += s_red[1][w];
     acc.x *= fall;
     acc.y *= fall;
     acc.z *= fall;
     acc.w *= fall;
-#pragma unroll
-    for (int i = 0; i < kMergeGroup; ++i) {
-      if (ml[i].y == 0.f) continue;  // no tokens
-      const float x = ml[i].x == M ? 1.f : ex2_fast(ml[i].x - M);
-      sum = fmaf(x, ml[i].y, sum);
-      acc.x = fmaf(x, v[i].x, acc.x);
-      acc.y = fmaf(x, v[i].y, acc.y);
-      acc.z = fmaf(x, v[i].z, acc.z);
-      acc.w = fmaf(x, v[i].w, acc.w);
+    const int m = min(n - s0, kMergeMax);
+#pragma unroll 8
+    for (int i = wid; i < m; i += kMergeWarps) {
+      const float wt = s_weight[i];
+      const int si = s0 + i;
+      const float4 v =
+          reinterpret_cast<const float4 *>(si < shared ? shared_o : a.o_part)
+              [place(si) * (kDim / 4) + lane];
+      if (wt == 0.f) continue;
+      acc.x = fmaf(wt, v.x, acc.x);
+      acc.y = fmaf(wt, v.y, acc.y);
+      acc.z = fmaf(wt, v.z, acc.z);
+      acc.w = fmaf(wt, v.w, acc.w);
     }
+    if (s0 + kMergeMax < n) __syncthreads();  // weights read
+  }
+  s_acc[wid][lane] = acc;
+  __syncthreads();
+  if (wid != 0) return;
+#pragma unroll
+  for (int w = 1; w < kMergeWarps; ++w) {
+    const float4 v = s_acc[w][lane];
+    acc.x += v.x;
+    acc.y += v.y;
+    acc.z += v.z;
+    acc.w += v.w;
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  reinterpret_cast<uint2 *>(a.o_out + row * kDim)[lane] = make_uint2(
+  reinterpret_cast<uint2 *>(a.o_out + (size_t)row * kDim)[lane] = make_uint2(
       pack_bf2q(acc.x * inv, acc.y * inv), pack_bf2q(acc.z * inv, acc.w * inv));
   if (lane == 0)
     a.lse_out[row] =
@@ -750,9 +780,7 @@ cudaError_t launch_qdecode(const void *q, const void *records,
   e = launch_pdl(kern, dim3((a.n_warps + kQdWarps - 1) / kQdWarps),
                  dim3(kQdThreads), qdecode_smem(false, batch), stream, a);
   if (e != cudaSuccess) return e;
-  const long long rows = units * G;
-  return launch_pdl(merge_kernel,
-                    dim3((unsigned)((rows + kMergeWarps - 1) / kMergeWarps)),
+  return launch_pdl(merge_kernel, dim3((unsigned)(units * G)),
                     dim3(32 * kMergeWarps), 0, stream, a, shared_o, shared_ml,
                     shared);
 }
