@@ -61,6 +61,9 @@ struct QdArgs {
   float2 *ml_part;   // [slot][G] (m, sum of weights)
   int *meta;         // run length, then the sequences' first positions
   int32_t *status;
+  // launched beside the kernel that takes the shared pages, which waited for
+  // everything before it: this one waits for it only before it ends
+  bool beside;
 };
 
 // pages of sequence b's own list, for lists that are not given
@@ -145,7 +148,7 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
     fence_mbar_init();
   }
   __syncwarp();
-  pdl_wait();
+  if (UNIT || !a.beside) pdl_wait();
   pdl_trigger();
 
   int total;
@@ -194,7 +197,10 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
           a.meta[1 + b] = s_pre[b];
     }
     const long long from = (long long)gw * chunk;
-    if (gw >= a.n_warps || from >= total) return;
+    if (gw >= a.n_warps || from >= total) {
+      if (a.beside) pdl_wait();
+      return;
+    }
     pb = (int)from;
     pe = min(total, pb + chunk);
   }
@@ -534,6 +540,7 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
     const int last = lists.unit(pe - 1);
     advance(last);
     flush(last);
+    if (a.beside) pdl_wait();
   } else {
     // the 4 C slices of the unit, merged head by head: CTA r of the cluster
     // takes heads r, r + C, .., its warp w every fourth of those; a lane
@@ -756,7 +763,7 @@ cudaError_t launch_qdecode(const void *q, const void *records,
            static_cast<const uint8_t *>(records),
            num_phys, pt, seq_lens, idx, k, batch, h_kv, G, max_pages, 0,
            prefix, prefix_pages, static_cast<__nv_bfloat16 *>(o_out), lse_out,
-           o_part, ml_part, meta, status};
+           o_part, ml_part, meta, status, shared > 0};
   const bool wide = G > 8;
   const long long units = (long long)batch * h_kv;
   const int ucl = idx ? unit_cluster(units, k) : 0;

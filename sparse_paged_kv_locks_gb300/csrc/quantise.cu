@@ -115,11 +115,16 @@ __global__ void __launch_bounds__(kQThreads)
                     const int32_t *__restrict__ pt, int batch, int max_pages,
                     int32_t *status) {
   pdl_wait();
+  // four tokens, then heads, then the next four: a warp has one head's rows of
+  // four tokens, mostly neighbours in a page, whose scale bytes are then one
+  // access (a byte at a time they took XX us of the YY)
   const int64_t row =
       (int64_t)blockIdx.x * kQRowsPerBlock + (threadIdx.x >> 3);
   const int j = threadIdx.x & 7;
-  const int64_t i = row / h_kv;  // token
-  const int h = (int)(row - i * h_kv);
+  const int64_t four = row / (4 * h_kv);
+  const int rest = (int)(row - four * (4 * h_kv));
+  const int64_t i = 4 * four + (rest & 3);  // token
+  const int h = rest >> 2;
   bool live = i < n_tokens;
   int64_t phys = 0;
   int slot = 0;
@@ -231,7 +236,7 @@ cudaError_t launch_quantise(const void *k_new, const void *v_new, int type,
   auto *kern = type == LOCKS_TYPE_BF16   ? quantise_kernel<LOCKS_TYPE_BF16>
                : type == LOCKS_TYPE_FP16 ? quantise_kernel<LOCKS_TYPE_FP16>
                                          : quantise_kernel<LOCKS_TYPE_FP32>;
-  const long long rows = (long long)n_tokens * h_kv;
+  const long long rows = ((long long)n_tokens + 3) / 4 * 4 * h_kv;
   const unsigned grid =
       (unsigned)((rows + kQRowsPerBlock - 1) / kQRowsPerBlock);
   return launch_pdl(kern, dim3(grid), dim3(kQThreads), 0, stream, k_new,
