@@ -116,8 +116,8 @@ __global__ void __launch_bounds__(kQThreads)
                     int32_t *status) {
   pdl_wait();
   // four tokens, then heads, then the next four: a warp has one head's rows of
-  // four tokens, mostly neighbours in a page, whose scale bytes are then one
-  // access (a byte at a time they took XX us of the YY)
+  // four tokens, mostly neighbours in a page, so that their scale bytes are
+  // one access
   const int64_t row =
       (int64_t)blockIdx.x * kQRowsPerBlock + (threadIdx.x >> 3);
   const int j = threadIdx.x & 7;
@@ -126,31 +126,32 @@ __global__ void __launch_bounds__(kQThreads)
   const int64_t i = 4 * four + (rest & 3);  // token
   const int h = rest >> 2;
   bool live = i < n_tokens;
-  int64_t phys = 0;
-  int slot = 0;
-  if (live) {
-    const int b = __ldg(seq_ids + i), pos = __ldg(positions + i);
-    if (b < 0) {  // padding
-      live = false;
-    } else if (b >= batch || pos < 0 || (pos >> 4) >= max_pages) {
-      if (j == 0) set_status(status, LOCKS_DEV_BAD_PAIR);
-      live = false;
-    } else {
-      phys = __ldg(pt + (size_t)b * max_pages + (pos >> 4));
-      slot = pos & 15;
-      if (phys < 0 || phys >= num_phys) {
-        if (j == 0) set_status(status, LOCKS_DEV_BAD_PAGE_ID);
-        live = false;
-      }
-    }
-  }
+  // the rows are on their way while their places are looked up
   float x[16], y[16];
+  int b = -1, pos = 0;
   if (live) {
+    b = __ldg(seq_ids + i);
+    pos = __ldg(positions + i);
     load16<TYPE>(k_new, i * k_token + h * k_head + 16 * j, x);
     load16<TYPE>(v_new, i * v_token + h * v_head + 16 * j, y);
   } else {
 #pragma unroll
     for (int t = 0; t < 16; ++t) x[t] = y[t] = 0.f;
+  }
+  int64_t phys = 0;
+  int slot = 0;
+  if (b < 0) {  // padding
+    live = false;
+  } else if (b >= batch || pos < 0 || (pos >> 4) >= max_pages) {
+    if (j == 0) set_status(status, LOCKS_DEV_BAD_PAIR);
+    live = false;
+  } else {
+    phys = __ldg(pt + (size_t)b * max_pages + (pos >> 4));
+    slot = pos & 15;
+    if (phys < 0 || phys >= num_phys) {
+      if (j == 0) set_status(status, LOCKS_DEV_BAD_PAGE_ID);
+      live = false;
+    }
   }
   uint8_t *rec = records + ((size_t)(live ? phys : 0) * h_kv + h) * kQRec;
   quantise_row(x, j, slot, rec, rec + kQOffKE, live);
