@@ -144,6 +144,19 @@ __device__ __forceinline__ void tm_st32(uint32_t addr,
       "r"(r[30]), "r"(r[31])
       : "memory");
 }
+// 32 columns of 16 lanes, as matrix fragments
+__device__ __forceinline__ void tm_ld16x256(uint32_t (&r)[16],
+                                            uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]),
+        "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
 // 16 columns
 __device__ __forceinline__ void tm_ld16(uint32_t (&r)[16], uint32_t addr) {
   asm volatile(
@@ -253,7 +266,7 @@ struct PfShared {
   uint32_t there[2];
   uint32_t tmem;
   int dead;
-  uint64_t k_raw, k_full, v_raw, v_read, v_full, info[2];
+  uint64_t q_full, k_raw, k_full, v_raw, v_read, v_full, info[2];
   uint64_t p_full, qk_done, pv_done, drain;
 };
 
@@ -315,6 +328,7 @@ __global__ void __launch_bounds__(kPfThreads, 2)
         "r"(kPfColumns)
         : "memory");
     if (lane == 0) {
+      mbar_init(&sh.q_full, 4);
       mbar_init(&sh.k_raw, 1);
       mbar_init(&sh.k_full, 1);
       mbar_init(&sh.v_raw, 1);
@@ -330,12 +344,15 @@ __global__ void __launch_bounds__(kPfThreads, 2)
       fence_mbar_init();
     }
   }
+  tm_fence_before();
+  __syncthreads();
+  tm_fence_after();
+  const uint32_t tm = sh.tmem;
   pdl_wait();
   pdl_trigger();
 
-  // the query rows: hi and lo codes, the scale that they leave to scores
-  float f = 0.f;
   if (wid < 4) {
+    // the query rows: hi and lo codes, the scale that they leave to scores
     const uint4 *src = reinterpret_cast<const uint4 *>(
         a.q + ((size_t)(row / a.G) * a.h_kv * a.G + (size_t)h * a.G +
                row % a.G) * kDim);
@@ -354,7 +371,7 @@ __global__ void __launch_bounds__(kPfThreads, 2)
     const int e =
         max(-100, (int)(tb >> 23) - 135 + ((tb & 0x7fffffu) > 0x600000u));
     const float down = exp2_int(-e);
-    f = exp2_int(e) * kPfScale;
+    const float f = exp2_int(e) * kPfScale;
 #pragma unroll 2
     for (int i = 0; i < 8; ++i) {  // 16 dims
       uint32_t hi[4], lo[4];
@@ -383,13 +400,8 @@ __global__ void __launch_bounds__(kPfThreads, 2)
       st_shared_v4(at + kPfQuery, make_uint4(lo[0], lo[1], lo[2], lo[3]));
     }
     fence_to_async();
-  }
-  tm_fence_before();
-  __syncthreads();
-  tm_fence_after();
-  const uint32_t tm = sh.tmem;
-
-  if (wid < 4) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.q_full);
     // ------------------------------------------------------------- softmax
     const uint32_t mine = tm + ((uint32_t)(wid * 32) << 16);
     float m = -INFINITY, l = 0.f;
@@ -499,25 +511,35 @@ __global__ void __launch_bounds__(kPfThreads, 2)
     if (ok) ok = pf_wait(sh, &sh.pv_done, (n - 1) & 1);
     ok = __all_sync(0xffffffffu, ok);
     tm_fence_after();
-    const size_t all = (size_t)rows * a.h_kv;
-    const size_t out = (size_t)split * all +
-                      (size_t)(row / a.G) * a.h_kv * a.G + (size_t)h * a.G +
-                      row % a.G;
-    for (int c = 0; c < 4; ++c) {
-      uint32_t o[32];
-      tm_ld32(o, mine + kPfColO + 32 * c);
-      tm_wait_ld();
-      if (row < rows && ok) {
-        float4 *dst =
-            reinterpret_cast<float4 *>(a.o_part + out * kDim) + 8 * c;
+    // partials: 16 rows at a time as matrix fragments (row lane / 4 and + 8,
+    // columns 2 (lane % 4), + 1 of every 8), so that four lanes write a whole
+    // memory sector
+    auto place = [&](int r) -> size_t {
+      return (size_t)split * rows * a.h_kv +
+             (size_t)(r / a.G) * a.h_kv * a.G + (size_t)h * a.G + r % a.G;
+    };
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          dst[i] = make_float4(
-              __uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-              __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+    for (int half = 0; half < 2; ++half) {
+      const int r0 = rt * kPfRows + 32 * wid + 16 * half + (lane >> 2);
+      float *d0 = a.o_part + place(r0) * kDim + 2 * (lane & 3);
+      float *d1 = a.o_part + place(r0 + 8) * kDim + 2 * (lane & 3);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[16];
+        tm_ld16x256(o, mine + ((uint32_t)(16 * half) << 16) + kPfColO + 32 * c);
+        tm_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (r0 < rows && ok)
+            *reinterpret_cast<float2 *>(d0 + 32 * c + 8 * i) = make_float2(
+                __uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]));
+          if (r0 + 8 < rows && ok)
+            *reinterpret_cast<float2 *>(d1 + 32 * c + 8 * i) = make_float2(
+                __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+        }
       }
     }
-    if (row < rows) a.ml_part[out] = make_float2(m, ok ? l : 0.f);
+    if (row < rows) a.ml_part[place(row)] = make_float2(m, ok ? l : 0.f);
   } else {
     auto good = [&](int ph) -> bool { return ph >= 0 && ph < a.num_phys; };
     // page lane & 7 of tile t as the table has it, -1 past the end
@@ -563,7 +585,8 @@ __global__ void __launch_bounds__(kPfThreads, 2)
       const uint64_t dv = mat_desc(v_s, kPfBlock);
       copy_values(ph);
       for (int j = 0; j < n; ++j) {
-        ok = pf_wait(sh, &sh.k_full, j & 1);
+        ok = (j > 0 || pf_wait(sh, &sh.q_full, 0)) &&
+             pf_wait(sh, &sh.k_full, j & 1);
         if (!__all_sync(0xffffffffu, ok)) break;
         tm_fence_after();
         if (elect_one()) {
@@ -615,16 +638,19 @@ __global__ void __launch_bounds__(kPfThreads, 2)
         for (int h2 = 0; h2 < 2; ++h2) {
           const uint32_t at = k_s + h2 * 4 * kQCodes +
                               (2 * (lane >> 2) + 1) * 128 + 16 * (lane & 3);
+          // rows that are read together start with different halves
+          const uint32_t a0 = at + (lane & 4 ? 64 : 0);
+          const uint32_t a1 = at + (lane & 4 ? 0 : 64);
           uint4 x[4], y[4];
 #pragma unroll
           for (int p = 0; p < 4; ++p) {
-            x[p] = lds128(at + p * kQCodes);
-            y[p] = lds128(at + p * kQCodes + 64);
+            x[p] = lds128(a0 + p * kQCodes);
+            y[p] = lds128(a1 + p * kQCodes);
           }
 #pragma unroll
           for (int p = 0; p < 4; ++p) {
-            st_shared_v4(at + p * kQCodes, y[p]);
-            st_shared_v4(at + p * kQCodes + 64, x[p]);
+            st_shared_v4(a0 + p * kQCodes, y[p]);
+            st_shared_v4(a1 + p * kQCodes, x[p]);
           }
         }
         fence_to_async();
@@ -755,9 +781,10 @@ __global__ void __launch_bounds__(kPfThreads, 2)
 // launcher
 // ---------------------------------------------------------------------------
 // How many ranges the prefix's tiles are cut into: enough CTAs for two to an
-// SM, and no more waves of them than pay.  A tile costs a CTA about 1.2 us,
-// its start and end 4 us, a split of one row 1 KB of traffic.  A rule on
-// sizes alone (152 SMs), so that the workspace's size needs no GPU.
+// SM, and no more waves of them than pay.  A tile costs a CTA about 2.6 us
+// with another beside it, its start and end 8 us, a row's partial 1 KB of
+// traffic.  A rule on sizes alone (152 SMs), so that the workspace's size
+// needs no GPU.
 int prefix_splits(int batch, int h_kv, int G, int pages) {
   const long long slots = 304;
   const long long row_tiles =
@@ -768,7 +795,7 @@ int prefix_splits(int batch, int h_kv, int G, int pages) {
   int splits = 1;
   for (long long s = 1; s <= tiles && s <= 64; ++s) {
     const double waves = (double)((base * s + slots - 1) / slots);
-    const double us = waves * (1.2 * (double)((tiles + s - 1) / s) + 4.0) +
+    const double us = waves * (2.6 * (double)((tiles + s - 1) / s) + 8.0) +
                       1.6e-4 * (double)(s * batch * h_kv * G);
     if (us < best * 0.999) {
       best = us;
