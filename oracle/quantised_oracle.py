@@ -105,16 +105,13 @@ def attend(q, K, V):
 
 def tokens(cache, table_row, h, pages, length, prefix=None):
     """Valid tokens of the listed pages of one sequence and head."""
-    ks, vs = [np.zeros((0, DIM))], [np.zeros((0, DIM))]
-    for pg in pages:
-        n = min(PAGE, length - PAGE * pg)
-        if pg < 0 or n <= 0:
-            continue
-        shared = prefix is not None and pg < len(prefix)
-        K, V = read(cache[prefix[pg] if shared else table_row[pg], h])
-        ks.append(K[:n])
-        vs.append(V[:n])
-    return np.concatenate(ks), np.concatenate(vs)
+    pages = np.asarray(list(pages), np.int64)
+    pages = pages[(pages >= 0) & (PAGE * pages < length)]
+    phys = np.array([prefix[p] if prefix is not None and p < len(prefix)
+                     else table_row[p] for p in pages], np.int64)
+    K, V = read(cache[phys, h].reshape(-1, RECORD))
+    keep = (PAGE * pages[:, None] + np.arange(PAGE) < length).reshape(-1)
+    return K.reshape(-1, DIM)[keep], V.reshape(-1, DIM)[keep]
 
 
 def decode(q, cache, page_table, seq_lens, idx=None, prefix=None):

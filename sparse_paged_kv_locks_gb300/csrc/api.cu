@@ -570,6 +570,7 @@ static PrefixRegion prefix_region(uint8_t *at, int batch, int h_q, int h_kv,
                                   int pages) {
   if (pages == 0 || batch == 0) return {0, nullptr, nullptr, 0};
   const int splits = prefix_splits(batch, h_kv, h_q / h_kv, pages);
+  if (splits == 0) return {0, nullptr, nullptr, 0};
   const size_t rows = (size_t)splits * batch * h_q;
   const size_t sums = round_up(rows * kDim * 4, 256);
   return {splits, reinterpret_cast<float *>(at),
@@ -614,7 +615,7 @@ locks_status_t locks_prefix_decode(
   const int G = h_q / h_kv;
   int32_t *status = reinterpret_cast<int32_t *>(ws);
   cudaError_t e = cudaSuccess;
-  if (prefix_pages > 0)
+  if (p.splits > 0)
     e = launch_prefix(q, records, num_phys_pages, prefix_table, prefix_pages,
                       batch, h_kv, G, p.splits, p.o_part, p.ml_part, status,
                       (cudaStream_t)stream);

@@ -194,7 +194,7 @@ cudaError_t launch_qdecode(const void *q, const void *records,
 int qdecode_max_batch();
 
 // attention of all query rows over the shared pages, in `splits` partials
-// (prefix.cu)
+// (prefix.cu; 0: not worth a kernel of its own)
 int prefix_splits(int batch, int h_kv, int G, int pages);
 cudaError_t launch_prefix(const void *q, const void *records,
                           int64_t num_phys, const int32_t *table, int pages,

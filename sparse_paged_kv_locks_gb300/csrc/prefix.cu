@@ -57,6 +57,8 @@ constexpr int kPfSmem =
 constexpr int kPfColumns = 256;             // tensor memory: S, then O
 constexpr int kPfColO = kPfTile;
 constexpr float kPfScale = 0.12751743074602467f;  // log2(e) / sqrt(128)
+// fewest (sequence, KV head, page) triples that are worth the kernel
+constexpr long long kPfMinShared = 24576;
 constexpr float kPfLift = 8.f;   // as in the single-token kernel
 constexpr float kPfSlack = 7.f;
 
@@ -785,7 +787,9 @@ __global__ void __launch_bounds__(kPfThreads, 2)
 // with another beside it, its start and end 8 us, a row's partial 1 KB of
 // traffic.  A rule on sizes alone (152 SMs), so that the workspace's size
 // needs no GPU.
+// 0: too little to share, every sequence reads the pages itself.
 int prefix_splits(int batch, int h_kv, int G, int pages) {
+  if ((long long)batch * h_kv * pages < kPfMinShared) return 0;
   const long long slots = 304;
   const long long row_tiles =
       ((long long)batch * G + kPfRows - 1) / kPfRows;

@@ -33,6 +33,15 @@ constexpr int kQdStages = 4;
 constexpr int kQdStride = 4224;  // ring stage: a record, 128-byte aligned
 constexpr int kQdWarpRing = kQdStages * kQdStride;
 constexpr int kQdRing = kQdWarps * kQdWarpRing;
+// Split form: fewest list entries to a warp, so that a unit is not cut into
+// more pieces than its merge is worth (2 units of 2,500 pages: 3 entries 39
+// us, 6 28 us, 12 24 us).  Beside the prefix kernel, after which this one
+// mostly runs and whose partials are merged anyhow, 2 (32K prefix for 32
+// sequences: 12 entries 65 us, 2 51 us).
+constexpr int kQdMinRun = 12, kQdMinRunBeside = 2;
+// unit form for lists that are not given: tables of at most this many pages
+// per CTA (a short sequence leaves its CTA idle, a long one would keep it)
+constexpr int kQdUnitPages = 64;
 constexpr float kQdScale = 0.12751743074602467f;  // log2(e) / sqrt(128)
 constexpr float kQdLn2 = 0.69314718055994531f;
 constexpr float kQdLift = 8.f;    // weights are 2^(.. - m + 8)
@@ -50,9 +59,7 @@ struct QdArgs {
   int64_t num_phys;
   const int32_t *pt, *seq_lens, *idx;
   int k, batch, h_kv, G, max_pages, n_warps;
-  // pages that every sequence begins with (null, 0: none); a sequence at
-  // least that long leaves them out of its list, a shorter one finds its
-  // pages there
+  // pages that every sequence begins with (null, 0: none)
   const int32_t *prefix;
   int prefix_pages;
   __nv_bfloat16 *o_out;
@@ -61,15 +68,16 @@ struct QdArgs {
   float2 *ml_part;   // [slot][G] (m, sum of weights)
   int *meta;         // run length, then the sequences' first positions
   int32_t *status;
-  // launched beside the kernel that takes the shared pages, which waited for
-  // everything before it: this one waits for it only before it ends
+  // launched beside the kernel that takes those pages, which waited for
+  // everything before it: sequences at least as long as they are leave them
+  // out of their lists, and this kernel waits for that one only at its end
   bool beside;
 };
 
 // pages of sequence b's own list, for lists that are not given
 __device__ __forceinline__ int own_pages(const QdArgs &a, int L) {
   const int n = (L + kPage - 1) / kPage;
-  return L >= a.prefix_pages * kPage ? n - a.prefix_pages : n;
+  return a.beside && L >= a.prefix_pages * kPage ? n - a.prefix_pages : n;
 }
 
 __device__ __forceinline__ QEntry q_resolve(const QdArgs &a,
@@ -99,11 +107,10 @@ __device__ __forceinline__ QEntry q_resolve(const QdArgs &a,
       set_status(a.status, LOCKS_DEV_BAD_INDEX);
       return e;
     }
-  } else if (a.prefix_pages) {
-    if (L >= a.prefix_pages * kPage)
-      pg += a.prefix_pages;
-    else
-      table = a.prefix;
+  } else {
+    if (a.beside && L >= a.prefix_pages * kPage) pg += a.prefix_pages;
+    if (pg >= n) return e;  // (unit form: lists as long as the table)
+    if (pg < a.prefix_pages) table = a.prefix;
   }
   if (!a.idx) ph = __ldg(table + pg);
   if (ph < 0 || ph >= a.num_phys) {
@@ -128,9 +135,9 @@ __device__ __forceinline__ uint32_t pack_bf2q(float lo, float hi) {
 }
 
 // NT: column tiles of 8 query heads (1: G <= 8, 2: G <= 16).
-// UNIT: lists of k entries each, one unit to a CTA or cluster, merged on
-// chip; otherwise every warp takes a run of positions and units that span
-// runs are merged by merge_kernel.
+// UNIT: lists of k entries each (the given ones, or k = max_pages), one unit
+// to a CTA or cluster, merged on chip; otherwise every warp takes a run of
+// positions and units that span runs are merged by merge_kernel.
 template <int NT, bool UNIT>
 __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
     qdecode_kernel(const QdArgs a) {
@@ -140,7 +147,8 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int h_q = a.h_kv * a.G;
-  const PageLists lists{s_pre, a.batch, a.h_kv, a.idx ? a.h_kv * a.k : 0};
+  const PageLists lists{s_pre, a.batch, a.h_kv,
+                        UNIT || a.idx ? a.h_kv * a.k : 0};
   uint64_t *bar = s_bar[wid];
   if (lane == 0) {
 #pragma unroll
@@ -151,8 +159,8 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
   if (UNIT || !a.beside) pdl_wait();
   pdl_trigger();
 
-  int total;
-  if (a.idx) {
+  int total = 0;
+  if (UNIT || a.idx) {
     total = a.batch * a.h_kv * a.k;
   } else {
     for (int b = threadIdx.x; b < a.batch; b += kQdThreads)
@@ -189,7 +197,8 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
     pb = unit0 * a.k + (int)((long long)sl * a.k / nsl);
     pe = unit0 * a.k + (int)((long long)(sl + 1) * a.k / nsl);
   } else {
-    chunk = (int)max(1LL, ((long long)total + a.n_warps - 1) / a.n_warps);
+    chunk = (int)max((long long)(a.beside ? kQdMinRunBeside : kQdMinRun),
+                     ((long long)total + a.n_warps - 1) / a.n_warps);
     if (blockIdx.x == 0) {  // for the merge
       if (threadIdx.x == 0) a.meta[0] = chunk;
       if (!a.idx)
@@ -306,7 +315,7 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
     bool whole = false;
     if constexpr (!UNIT) {
       const int2 sp = lists.span(u);
-      whole = !a.prefix_pages && sp.x >= pb && sp.y <= pe;
+      whole = !a.beside && sp.x >= pb && sp.y <= pe;
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -612,13 +621,13 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
 // ---------------------------------------------------------------------------
 // merge of partials
 // ---------------------------------------------------------------------------
-// A CTA per (sequence, query head) row, its warps every fourth partial, four
+// A CTA per (sequence, query head) row, its warps every eighth partial, four
 // dims to a lane: the pieces that the runs left of the row's unit, and before
 // them the partials of the shared prefix where there is one (`shared` of them,
 // [split][batch * h_q], skipped by sequences shorter than the prefix).  The
 // references come first, all at once (a thread each), so that the sums' loads
 // depend on nothing and are in flight together.
-constexpr int kMergeWarps = 4;
+constexpr int kMergeWarps = 8;
 constexpr int kMergeMax = 32 * kMergeWarps;  // partials weighed at a time
 
 __global__ void __launch_bounds__(32 * kMergeWarps)
@@ -639,7 +648,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   if (sp.y > sp.x) {
     w0 = sp.x / chunk;
     own = (sp.y - 1) / chunk - w0 + 1;
-    if (own == 1 && !a.prefix_pages) return;  // written by its warp
+    if (own == 1 && !a.beside) return;  // written by its warp
   }
   if (shared) {
     const int L = checked_len(a.seq_lens, b, a.max_pages, nullptr);
@@ -747,7 +756,7 @@ static int unit_cluster(long long units, int k) {
   if (units >= sms) return 1;
   for (int c = 8; c >= 2; c >>= 1)
     if (units * c <= 2LL * sms && k >= c * kQdWarps) return c;
-  return 0;
+  return k <= 2 * kQdWarps ? 1 : 0;
 }
 
 cudaError_t launch_qdecode(const void *q, const void *records,
@@ -766,7 +775,9 @@ cudaError_t launch_qdecode(const void *q, const void *records,
            o_part, ml_part, meta, status, shared > 0};
   const bool wide = G > 8;
   const long long units = (long long)batch * h_kv;
-  const int ucl = idx ? unit_cluster(units, k) : 0;
+  if (!idx) a.k = max_pages;
+  int ucl = shared > 0 ? 0 : unit_cluster(units, a.k);
+  if (!idx && max_pages > kQdUnitPages * ucl) ucl = 0;
   if (ucl > 0) {
     cudaError_t e = wide ? qdecode_ready<2, true>() : qdecode_ready<1, true>();
     if (e != cudaSuccess) return e;

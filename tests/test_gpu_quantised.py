@@ -231,7 +231,9 @@ def test_read_stops_at_lengths_and_reports_bad_pairs():
 # ---------------------------------------------------------------------------
 # attention
 # ---------------------------------------------------------------------------
-def check(got_o, got_lse, q, rec, want):
+def check(got_o, got_lse, q, rec, want, below=0.0):
+    """`below`: what weights too small for fp16 may add up to (where one
+    token takes nearly all of a row, dims in which its value is zero)."""
     o, lse, mass = want
     got_o = got_o.double().cpu().numpy()
     got_lse = got_lse.double().cpu().numpy()
@@ -245,7 +247,7 @@ def check(got_o, got_lse, q, rec, want):
     dx = 2.0 ** -17 * np.abs(q).sum(-1) * kmax / math.sqrt(128)
     tol = 2.0 ** -8 * np.abs(o) + \
         (2.0 ** -11 + 2.0 ** -13 + 2 * dx[..., None]) * mass
-    bad = np.abs(got_o - o) > tol + 1e-30
+    bad = np.abs(got_o - o) > tol + 1e-30 + below
     assert not bad.any(), (np.argwhere(bad)[:5], got_o[bad][:5], o[bad][:5])
     ltol = dx + 2.0 ** -20 * np.abs(np.where(empty, 0, lse)) + 2.0 ** -20
     assert (np.abs(np.where(empty, 0, got_lse) - np.where(empty, 0, lse))
@@ -310,6 +312,34 @@ def test_dense_decode(G, lens, h_kv):
     assert st == 0
     qn = q.double().numpy()
     check(o, lse, qn, rec, Q.decode(qn, rec, table, lens))
+
+
+@pytest.mark.parametrize("G", [1, 4, 8, 16])
+@pytest.mark.parametrize("lens,h_kv,room", [
+    ([9000, 100, 0, 16], 1, 0), ([333, 1, 0, 90, 31], 3, 700),
+    ([0, 0], 2, 900), ([4000, 3990, 17], 2, 600)])
+def test_dense_decode_over_long_tables(G, lens, h_kv, room):
+    # tables too long for one unit to a CTA: runs over all lists, units that
+    # span many runs, runs that span many units, units of no pages
+    rng = np.random.default_rng(G + room)
+    rec, table = case(rng, lens, h_kv, room=room)
+    q = queries(rng, len(lens), G * h_kv)
+    o, lse, st = run_decode(q, rec, table, lens)
+    assert st == 0
+    qn = q.double().numpy()
+    check(o, lse, qn, rec, Q.decode(qn, rec, table, lens))
+
+
+def test_dense_decode_of_many_units():
+    rng = np.random.default_rng(21)
+    lens = [int(x) for x in rng.integers(0, 1100, 90)]
+    for room in (0, 300):          # one CTA to a unit, and runs
+        rec, table = case(rng, lens, 2, room=room)
+        q = queries(rng, 90, 10)
+        o, lse, st = run_decode(q, rec, table, lens)
+        assert st == 0
+        qn = q.double().numpy()
+        check(o, lse, qn, rec, Q.decode(qn, rec, table, lens))
 
 
 @pytest.mark.parametrize("G", [1, 4, 5, 8, 16])
@@ -503,19 +533,108 @@ def test_prefix(G, np_, lens, h_kv):
     check(o, lse, qn, rec, Q.decode(qn, rec, table, lens, prefix=prefix))
 
 
-@pytest.mark.parametrize("batch,G,h_kv,np_", [(33, 4, 2, 70), (70, 8, 1, 20),
-                                              (9, 16, 3, 130)])
+# enough pages times units that the prefix is taken once for all
+SHARED = [(256, 1, 8, 12), (240, 2, 8, 13), (31, 16, 4, 200), (6, 5, 8, 515),
+          (2, 8, 8, 1543), (64, 4, 1, 400), (100, 3, 3, 83)]
+
+
+@pytest.mark.parametrize("batch,G,h_kv,np_", [
+    (33, 4, 2, 70), (70, 8, 1, 20), (9, 16, 3, 130)] + SHARED)
 def test_prefix_of_many_rows(batch, G, h_kv, np_):
-    # several tiles of query rows, several splits of the prefix
+    # several tiles of query rows, several splits of the prefix, partial tiles
+    # of both; some sequences shorter than the prefix, one empty
     rng = np.random.default_rng(batch)
     lens = [16 * np_ + int(x) for x in rng.integers(0, 60, batch)]
     lens[batch // 2] = 16 * np_ - 3
+    lens[0] = 0 if batch > 20 else 16 * np_
     rec, prefix, table = prefix_case(rng, np_, lens, h_kv)
     q = queries(rng, batch, G * h_kv)
     o, lse, st = run_prefix(q, rec, prefix, table, lens)
     assert st == 0
     qn = q.double().numpy()
     check(o, lse, qn, rec, Q.decode(qn, rec, table, lens, prefix=prefix))
+
+
+@pytest.mark.parametrize("kind", ["strong", "scales", "rising", "large q",
+                                  "small q"])
+def test_shared_prefix_extremes(kind):
+    batch, G, h_kv, np_ = 31, 4, 4, 200
+    rng = np.random.default_rng(len(kind))
+    lens = [16 * np_ + int(x) for x in rng.integers(0, 20, batch)]
+    rec, prefix, table = prefix_case(rng, np_, lens, h_kv)
+    q = queries(rng, batch, G * h_kv,
+                {"large q": 1e15, "small q": 1e-25}.get(kind, 1.0))
+    if kind == "large q":          # .. against keys that undo it
+        rec[prefix, :, 4096:4112] = 127 - 32
+        rec[table[:, np_:][table[:, np_:] >= 0], :, 4096:4112] = 127 - 32
+        q = (q.float() * 2.0 ** -26).to(torch.bfloat16)
+    if kind == "strong":           # for one row of queries, in the prefix
+        r = rec[prefix[111]]
+        for h in range(h_kv):
+            codes, e = Q.quantise_rows(
+                4 * q[7, G * h:G * h + 1].double().numpy())
+            r[h, Q._PLACE[5]] = codes[0]
+            r[h, 4096 + 5] = e[0] + 127
+    if kind == "scales":           # rows of very different scales in a page
+        e = rec[prefix][..., 4096:].astype(np.int64)
+        e[..., :16] = 127 - 9 + rng.integers(-3, 4, e[..., :16].shape)
+        e[..., 16:] = 127 + rng.integers(-7, 8, e[..., 16:].shape)
+        tmp = rec[prefix]
+        tmp[..., 4096:] = e.astype(np.uint8)
+        rec[prefix] = tmp
+    if kind == "rising":           # scores rise along the prefix
+        codes, _ = Q.quantise_rows(np.full((1, 128), 448.0))
+        for i, p in enumerate(prefix):
+            for s in range(16):
+                rec[p, :, Q._PLACE[s]] = codes[0][:, None]
+                rec[p, :, 4096 + s] = 127 - 29 + i // 10
+        q = torch.ones_like(q)
+    o, lse, st = run_prefix(q, rec, prefix, table, lens)
+    assert st == 0
+    qn = q.double().numpy()
+    # weights are off by at most 2^-25 where the largest is 2^8 or more, times
+    # codes up to 448 and the largest value scale (2^-7), in each of the tokens
+    below = max(lens) * 2.0 ** -33 * 448 * 2.0 ** -7 if kind == "strong" else 0
+    check(o, lse, qn, rec, Q.decode(qn, rec, table, lens, prefix=prefix),
+          below)
+
+
+def test_shared_prefix_reports_bad_pages():
+    batch, G, h_kv, np_ = 31, 4, 4, 203
+    rng = np.random.default_rng(22)
+    lens = [16 * np_ + int(x) for x in rng.integers(0, 20, batch)]
+    rec, prefix, table = prefix_case(rng, np_, lens, h_kv)
+    q = queries(rng, batch, G * h_kv)
+    qn = q.double().numpy()
+    bad = prefix.copy()
+    gone = [0, 9, 17] + list(range(64, 72)) + [202]
+    bad[gone] = [-1, rec.shape[0], 2 ** 31 - 1] + [-5] * 8 + [rec.shape[0]]
+    # the poison of a page left out must not reach anything
+    rec[prefix[gone]] = 0x7F
+    o, lse, st = run_prefix(q, rec, bad, table, lens)
+    assert st == B.DEV_BAD_PAGE_ID
+    idx = np.tile(np.arange(np_ + 2, dtype=np.int32), (batch, h_kv, 1))
+    idx[:, :, gone] = -1
+    check(o, lse, qn, rec, Q.decode(qn, rec, table, lens, idx, prefix))
+
+
+def test_shared_prefix_does_not_mix_rows():
+    # NaN queries of one sequence, and NaN keys of one head, stay there
+    batch, G, h_kv, np_ = 31, 4, 4, 200
+    rng = np.random.default_rng(23)
+    lens = [16 * np_ + 5] * batch
+    rec, prefix, table = prefix_case(rng, np_, lens, h_kv)
+    rec[prefix[70], 2, Q._PLACE[3]] = 0x7F
+    q = queries(rng, batch, G * h_kv)
+    q[9, 4:8] = float("nan")
+    o, lse, st = run_prefix(q, rec, prefix, table, lens)
+    assert st == 0
+    nan = torch.isnan(lse).cpu()
+    want = torch.zeros_like(nan)
+    want[:, 8:12] = True
+    want[9, 4:8] = True
+    assert torch.equal(nan, want)
+    assert torch.equal(torch.isnan(o).any(-1).cpu(), want)
 
 
 def test_prefix_with_one_strong_token():
