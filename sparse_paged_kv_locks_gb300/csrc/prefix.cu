@@ -30,13 +30,20 @@
 // tile j runs.  Two CTAs fit an SM, with their columns of tensor memory fill
 // it, and one's softmax runs under the other's products.
 //
-// (Loads to registers instead of bulk copies stalled their warps for 2000 to
-// 3000 cycles a tile: the pages lie far apart, and the proxy fence before a
-// product waits for its thread's loads.  Copies of single rows to their
-// swizzled places took 7000 cycles a tile to issue.  Tiles of 64 tokens with two or
-// three buffers of everything, and so the products of one tile under the
-// softmax of the next, were slower, 335 us against 2XX on the 128K prefix:
-// a product reads the query from shared memory for half as many columns.)
+// Bound: for many rows, the chain scores -> softmax -> weights -> products of a
+// tile, about 4,800 cycles with another CTA's beside it (softmax 2,600, the
+// two products 1,100, the rest waits between the roles); tensor cores, special
+// functions and shared memory are each below two thirds.  With the softmax
+// left out a 128K prefix for 64 sequences and 64 query heads took 230 us, with
+// the products as well 205, against 303; without the exponentials 290.  For
+// few rows, the bytes of the records.  What was slower on that prefix: loads
+// to registers instead of bulk copies (the pages lie far apart, and the proxy
+// fence before a product waits for its thread's loads; 610 us), copies of
+// single rows to their swizzled places (850 us), three warps that each do a
+// third of everything (348 us), tiles of 64 tokens with two or three buffers
+// of everything (335 us: a product then reads the query from shared memory for
+// half as many columns), two threads to a row in eight softmax warps of 96
+// registers (347 us).
 #include "launch.h"
 #include "quantised.cuh"
 
@@ -373,7 +380,9 @@ __global__ void __launch_bounds__(kPfThreads, 2)
     const int e =
         max(-100, (int)(tb >> 23) - 135 + ((tb & 0x7fffffu) > 0x600000u));
     const float down = exp2_int(-e);
-    const float f = exp2_int(e) * kPfScale;
+    // codes have no infinity: a row that holds one has scores that are not
+    // numbers
+    const float f = isinf(top) ? top - top : exp2_int(e) * kPfScale;
 #pragma unroll 2
     for (int i = 0; i < 8; ++i) {  // 16 dims
       uint32_t hi[4], lo[4];
@@ -552,7 +561,8 @@ __global__ void __launch_bounds__(kPfThreads, 2)
     auto pages_there = [&](int ph) -> uint32_t {
       return __ballot_sync(0xffffffffu, good(ph)) & ((1u << kPfPages) - 1);
     };
-    // keys, or values and scales, of a tile's pages (ph: page lane & 7)
+    // keys, or values and scales, of a tile's pages (ph: page lane & 7); one
+    // arrival for all, a lane to a page
     auto copy = [&](int ph, int off, uint32_t bytes, uint32_t to,
                     uint64_t *bar) {
       const uint32_t there = pages_there(ph);
@@ -563,7 +573,6 @@ __global__ void __launch_bounds__(kPfThreads, 2)
                   a.records + ((size_t)ph * a.h_kv + h) * kQRec + off, bytes,
                   bar);
       __syncwarp();
-      return there;
     };
     // pages of tiles j, j + 1
     int ph = page(t0), ph_next = page(t0 + 1);
@@ -664,8 +673,8 @@ __global__ void __launch_bounds__(kPfThreads, 2)
       ok = __all_sync(0xffffffffu, ok);
       if (ok) mend_keys();
       for (int j = 0; j < n && ok; ++j) {
-        // what softmax needs to know of tile j (S(j - 1) is
-        // done, so O(j - 2) is, and the softmax that knew of j - 2)
+        // what softmax needs to know of tile j (S(j - 1) is done, so O(j - 2)
+        // is, and the softmax that was told of j - 2)
         ok = pf_wait(sh, &sh.v_raw, j & 1);
         if (!__all_sync(0xffffffffu, ok)) break;
         const uint32_t there = pages_there(ph);
@@ -786,8 +795,10 @@ __global__ void __launch_bounds__(kPfThreads, 2)
 // SM, and no more waves of them than pay.  A tile costs a CTA about 2.6 us
 // with another beside it, its start and end 8 us, a row's partial 1 KB of
 // traffic.  A rule on sizes alone (152 SMs), so that the workspace's size
-// needs no GPU.
-// 0: too little to share, every sequence reads the pages itself.
+// needs no GPU.  0: too little to share, every sequence reads the pages itself
+// (8 sequences, 8 KV heads: 128 pages 13.5 against 23 us, 512 pages 30.5
+// against 26; 32 and 8: 32 pages 12.3 against 24.5, 128 pages 30.7 against 26;
+// 64 and 8, G = 8: 32 pages 21 against 37, 128 pages 54 against 43).
 int prefix_splits(int batch, int h_kv, int G, int pages) {
   if ((long long)batch * h_kv * pages < kPfMinShared) return 0;
   const long long slots = 304;

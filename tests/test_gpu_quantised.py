@@ -695,26 +695,28 @@ def test_prefix_reports_bad_data():
 # ---------------------------------------------------------------------------
 # streams, graphs, the whole path
 # ---------------------------------------------------------------------------
-def test_other_stream_and_repeated_calls():
+@pytest.mark.parametrize("np_,batch", [(10, 2), (200, 62)])
+def test_other_stream_and_repeated_calls(np_, batch):
     rng = np.random.default_rng(17)
-    np_, lens = 10, [170, 300]
+    lens = [16 * np_ + int(x) for x in rng.integers(0, 150, batch)]
     rec, prefix, table = prefix_case(rng, np_, lens, 2)
-    q = queries(rng, 2, 8)
+    q = queries(rng, batch, 8)
     o, lse, _ = run_prefix(q, rec, prefix, table, lens)
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
-    ws = B.new_prefix_workspace(2, 8, 2, table.shape[1], np_, DEV)
+    ws = B.new_prefix_workspace(batch, 8, 2, table.shape[1], np_, DEV)
     s.wait_stream(torch.cuda.current_stream())
     for _ in range(3):                 # a used workspace, another stream
         o2, lse2, st = run_prefix(q, rec, prefix, table, lens, s, ws)
         assert st == 0 and torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
-def test_step_as_a_graph():
+@pytest.mark.parametrize("np_,batch", [(9, 3), (200, 62)])
+def test_step_as_a_graph(np_, batch):
     # write one token per sequence, then attend, replayed with new inputs
     rng = np.random.default_rng(18)
-    batch, h_kv, G, np_ = 3, 2, 4, 9
-    lens = np.array([150, 144, 201])
+    h_kv, G = 2, 4
+    lens = 16 * np_ + rng.integers(0, 60, batch)
     rec, prefix, table = prefix_case(rng, np_, [int(x) + 3 for x in lens],
                                      h_kv)
     cache = torch.from_numpy(rec).to(DEV)
@@ -782,3 +784,27 @@ def test_summaries_from_pages_read_back():
     b = O.decode_records(np.asarray(ostore).reshape(-1, 832))
     for part in ("mu8", "smu"):
         np.testing.assert_array_equal(a[part], b[part])
+
+
+def test_example_runs_them_together():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(
+        os.path.abspath(__file__))), "examples", "quantised_cache.py")
+    spec = importlib.util.spec_from_file_location("quantised_cache", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    # some pages selected, then all: where the lists hold every page the two
+    # attentions are the same sums, each rounded to bf16 once (2^-8 of the
+    # value apiece) after weights of 2^-11
+    s, mass = example.main(batch=4, h_q=8, h_kv=2, doc_pages=40, k=12,
+                           steps=20, show=lambda _: None)
+    assert s.bad() == 0 and 0.1 < mass < 1.0
+    s, mass = example.main(batch=4, h_q=8, h_kv=2, doc_pages=40, k=50,
+                           steps=17, show=lambda _: None)
+    assert s.bad() == 0
+    (o, lse), (o2, lse2) = s.outs
+    K, V = Q.read(s.cache.cpu().numpy())
+    tol = 2.0 ** -7 * o.abs().max() + 2.0 ** -10 * float(np.abs(V).max())
+    assert (o.float() - o2.float()).abs().max() <= tol
+    assert (lse - lse2).abs().max() <= 1e-4
