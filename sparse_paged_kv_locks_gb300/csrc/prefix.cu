@@ -43,7 +43,9 @@
 // third of everything (348 us), tiles of 64 tokens with two or three buffers
 // of everything (335 us: a product then reads the query from shared memory for
 // half as many columns), two threads to a row in eight softmax warps of 96
-// registers (347 us).
+// registers (347 us), the scores of the next tile's first half under the
+// softmax of this one's second (two buffers of keys, products of 64 columns;
+// 323 us: every role then ran slower beside the others).
 #include "launch.h"
 #include "quantised.cuh"
 

@@ -626,39 +626,53 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
 // ---------------------------------------------------------------------------
 // merge of partials
 // ---------------------------------------------------------------------------
-// A CTA per (sequence, query head) row, its warps every eighth partial, four
-// dims to a lane: the pieces that the runs left of the row's unit, and before
-// them the partials of the shared prefix where there is one (`shared` of them,
+// W warps to a (sequence, query head) row, each every W-th partial, four dims
+// to a lane: the pieces that the runs left of the row's unit, and before them
+// the partials of the shared prefix where there is one (`shared` of them,
 // [split][batch * h_q], skipped by sequences shorter than the prefix).  The
 // references come first, all at once (a thread each), so that the sums' loads
-// depend on nothing and are in flight together.
+// depend on nothing and are in flight together.  Bound by the latency of these
+// three rounds of loads, and by the partials' bytes where rows are many: W is
+// the most that keeps all rows' warps resident in two waves (4,096 rows of some
+// 23 partials, caches cold: 8 warps 28 us, 2 warps 25 us; 16 rows of 200, as
+// part of their call: 4 warps 39 us, 8 warps 28 us).
 constexpr int kMergeWarps = 8;
-constexpr int kMergeMax = 32 * kMergeWarps;  // partials weighed at a time
 
+template <int W>
 __global__ void __launch_bounds__(32 * kMergeWarps)
     merge_kernel(const QdArgs a, const float *__restrict__ shared_o,
                  const float2 *__restrict__ shared_ml, int shared) {
-  __shared__ float s_weight[kMergeMax], s_red[2][kMergeWarps];
+  constexpr int kAtOnce = 32 * W;  // partials weighed at a time
+  __shared__ float s_weight[32 * kMergeWarps], s_red[2][kMergeWarps];
   __shared__ float4 s_acc[kMergeWarps][32];
   pdl_wait();
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  const int rows = a.batch * a.h_kv * a.G, row = blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int group = warp / W, wid = warp % W, first = group * W;
+  const int in_group = wid * 32 + lane;
+  const int rows = a.batch * a.h_kv * a.G;
+  const int row = blockIdx.x * (kMergeWarps / W) + group;
+  if (row >= rows) return;
+  auto sync = [&]() {  // the row's warps
+    if constexpr (W == 1)
+      __syncwarp();
+    else
+      asm volatile("bar.sync %0, %1;\n" ::"r"(1 + group), "n"(32 * W)
+                   : "memory");
+  };
   const int u = row / a.G, hd = row - u * a.G;
   const int b = u / a.h_kv;
   const PageLists lists{a.meta + 1, a.batch, a.h_kv,
                         a.idx ? a.h_kv * a.k : 0};
   const int chunk = a.meta[0];
   const int2 sp = lists.span(u);
+  const int L = shared ? checked_len(a.seq_lens, b, a.max_pages, nullptr) : 0;
   int w0 = 0, own = 0;
   if (sp.y > sp.x) {
     w0 = sp.x / chunk;
     own = (sp.y - 1) / chunk - w0 + 1;
     if (own == 1 && !a.beside) return;  // written by its warp
   }
-  if (shared) {
-    const int L = checked_len(a.seq_lens, b, a.max_pages, nullptr);
-    if (L < a.prefix_pages * kPage) shared = 0;
-  }
+  if (L < a.prefix_pages * kPage) shared = 0;
   const int n = shared + own;
   auto place = [&](int s) -> size_t {
     return s < shared ? (size_t)s * rows + row
@@ -666,19 +680,21 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   };
   float M = -INFINITY, sum = 0.f;  // the same in all threads
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);  // this warp's share
-  for (int s0 = 0; s0 < n; s0 += kMergeMax) {
-    const int s = s0 + threadIdx.x;
+  for (int s0 = 0; s0 < n; s0 += kAtOnce) {
+    const int s = s0 + in_group;
     float2 ml = make_float2(-INFINITY, 0.f);
     if (s < n) ml = (s < shared ? shared_ml : a.ml_part)[place(s)];
     float top = ml.x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1)
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) s_red[0][wid] = top;
-    __syncthreads();
-    top = M;
+    if (W > 1) {
+      if (lane == 0) s_red[0][warp] = top;
+      sync();
 #pragma unroll
-    for (int w = 0; w < kMergeWarps; ++w) top = fmaxf(top, s_red[0][w]);
+      for (int w = 0; w < W; ++w) top = fmaxf(top, s_red[0][first + w]);
+    }
+    top = fmaxf(top, M);
     const float fall = M == top ? 1.f : ex2_fast(M - top);
     M = top;
     // nothing from a partial without tokens; one whose scores are not
@@ -688,20 +704,23 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1)
       part += __shfl_xor_sync(0xffffffffu, part, o);
-    if (lane == 0) s_red[1][wid] = part;
-    s_weight[threadIdx.x] = x;
-    __syncthreads();
-    sum *= fall;
+    if (W > 1 && lane == 0) s_red[1][warp] = part;
+    s_weight[first * 32 + in_group] = x;
+    sync();
+    if (W > 1) {
+      part = 0.f;
 #pragma unroll
-    for (int w = 0; w < kMergeWarps; ++w) sum += s_red[1][w];
+      for (int w = 0; w < W; ++w) part += s_red[1][first + w];
+    }
+    sum = sum * fall + part;
     acc.x *= fall;
     acc.y *= fall;
     acc.z *= fall;
     acc.w *= fall;
-    const int m = min(n - s0, kMergeMax);
+    const int m = min(n - s0, kAtOnce);
 #pragma unroll 8
-    for (int i = wid; i < m; i += kMergeWarps) {
-      const float wt = s_weight[i];
+    for (int i = wid; i < m; i += W) {
+      const float wt = s_weight[first * 32 + i];
       const int si = s0 + i;
       const float4 v =
           reinterpret_cast<const float4 *>(si < shared ? shared_o : a.o_part)
@@ -712,18 +731,20 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
       acc.z = fmaf(wt, v.z, acc.z);
       acc.w = fmaf(wt, v.w, acc.w);
     }
-    if (s0 + kMergeMax < n) __syncthreads();  // weights read
+    if (s0 + kAtOnce < n) sync();  // weights read
   }
-  s_acc[wid][lane] = acc;
-  __syncthreads();
-  if (wid != 0) return;
+  if (W > 1) {
+    s_acc[warp][lane] = acc;
+    sync();
+    if (wid != 0) return;
 #pragma unroll
-  for (int w = 1; w < kMergeWarps; ++w) {
-    const float4 v = s_acc[w][lane];
-    acc.x += v.x;
-    acc.y += v.y;
-    acc.z += v.z;
-    acc.w += v.w;
+    for (int w = 1; w < W; ++w) {
+      const float4 v = s_acc[first + w][lane];
+      acc.x += v.x;
+      acc.y += v.y;
+      acc.z += v.z;
+      acc.w += v.w;
+    }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   reinterpret_cast<uint2 *>(a.o_out + (size_t)row * kDim)[lane] = make_uint2(
@@ -803,9 +824,18 @@ cudaError_t launch_qdecode(const void *q, const void *records,
   e = launch_pdl(kern, dim3((a.n_warps + kQdWarps - 1) / kQdWarps),
                  dim3(kQdThreads), qdecode_smem(false, batch), stream, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(merge_kernel, dim3((unsigned)(units * G)),
-                    dim3(32 * kMergeWarps), 0, stream, a, shared_o, shared_ml,
-                    shared);
+  const long long rows = units * G;
+  const long long room = 32LL * device_sm_count();
+  auto merge = [&](auto *kern, int w) {
+    const int per = kMergeWarps / w;
+    return launch_pdl(kern, dim3((unsigned)((rows + per - 1) / per)),
+                      dim3(32 * kMergeWarps), 0, stream, a, shared_o,
+                      shared_ml, shared);
+  };
+  if (rows * 8 <= 2 * room) return merge(merge_kernel<8>, 8);
+  if (rows * 4 <= 2 * room) return merge(merge_kernel<4>, 4);
+  if (rows * 2 <= 2 * room) return merge(merge_kernel<2>, 2);
+  return merge(merge_kernel<1>, 1);
 }
 
 }  // namespace locks
