@@ -797,12 +797,16 @@ __global__ void __launch_bounds__(kPfThreads, 2)
 // SM, and no more waves of them than pay.  A tile costs a CTA about 2.6 us
 // with another beside it, its start and end 8 us, a row's partial 1 KB of
 // traffic.  A rule on sizes alone (152 SMs), so that the workspace's size
-// needs no GPU.  0: too little to share, every sequence reads the pages itself
-// (8 sequences, 8 KV heads: 128 pages 13.5 against 23 us, 512 pages 30.5
-// against 26; 32 and 8: 32 pages 12.3 against 24.5, 128 pages 30.7 against 26;
-// 64 and 8, G = 8: 32 pages 21 against 37, 128 pages 54 against 43).
+// needs no GPU.
+//
+// 0: too little to share, every sequence reads the pages itself.  (Sequences,
+// KV heads, pages, G = 4 unless given: read by each against once.)  8, 8, 128:
+// 13.5 and 23 us; 8, 8, 512: 30.5 and 26; 2, 8, 1024: 24.6 and 24.4; 2, 8,
+// 4096: 49 and 47; 32, 8, 32: 12.3 and 24.5; 32, 8, 128: 31 and 26; 64, 8, 32,
+// G = 8: 21 and 37; 16, 8, 256, G = 16: 41 and 30; 256, 8, 12, G = 1: 31.5 and
+// 26; 128, 1, 512, G = 8: 46 and 28; one sequence, 8, 8192: 64 and 77.
 int prefix_splits(int batch, int h_kv, int G, int pages) {
-  if ((long long)batch * h_kv * pages < kPfMinShared) return 0;
+  if (batch < 2 || (long long)batch * h_kv * pages < kPfMinShared) return 0;
   const long long slots = 304;
   const long long row_tiles =
       ((long long)batch * G + kPfRows - 1) / kPfRows;
