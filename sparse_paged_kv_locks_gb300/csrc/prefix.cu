@@ -804,7 +804,9 @@ __global__ void __launch_bounds__(kPfThreads, 2)
 // 13.5 and 23 us; 8, 8, 512: 30.5 and 26; 2, 8, 1024: 24.6 and 24.4; 2, 8,
 // 4096: 49 and 47; 32, 8, 32: 12.3 and 24.5; 32, 8, 128: 31 and 26; 64, 8, 32,
 // G = 8: 21 and 37; 16, 8, 256, G = 16: 41 and 30; 256, 8, 12, G = 1: 31.5 and
-// 26; 128, 1, 512, G = 8: 46 and 28; one sequence, 8, 8192: 64 and 77.
+// 26; 128, 1, 512, G = 8: 46 and 28; one sequence, 8, 8192: 64 and 77.  A long
+// prefix of one KV head (4, 1, 8192, G = 16: 48 and 34) takes all 304 ranges;
+// with 64 at most it took 43.
 int prefix_splits(int batch, int h_kv, int G, int pages) {
   if (batch < 2 || (long long)batch * h_kv * pages < kPfMinShared) return 0;
   const long long slots = 304;
@@ -814,7 +816,7 @@ int prefix_splits(int batch, int h_kv, int G, int pages) {
   const long long tiles = (pages + kPfPages - 1) / kPfPages;
   double best = 1e30;
   int splits = 1;
-  for (long long s = 1; s <= tiles && s <= 64; ++s) {
+  for (long long s = 1; s <= tiles && s <= slots; ++s) {
     const double waves = (double)((base * s + slots - 1) / slots);
     const double us = waves * (2.6 * (double)((tiles + s - 1) / s) + 8.0) +
                       1.6e-4 * (double)(s * batch * h_kv * G);

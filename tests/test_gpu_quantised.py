@@ -539,7 +539,8 @@ SHARED = [(256, 1, 8, 12), (240, 2, 8, 13), (31, 16, 4, 200), (6, 5, 8, 515),
 
 
 @pytest.mark.parametrize("batch,G,h_kv,np_", [
-    (33, 4, 2, 70), (70, 8, 1, 20), (9, 16, 3, 130)] + SHARED)
+    (33, 4, 2, 70), (70, 8, 1, 20), (9, 16, 3, 130), (1, 4, 8, 3100),
+    (5, 16, 1, 7001)] + SHARED)
 def test_prefix_of_many_rows(batch, G, h_kv, np_):
     # several tiles of query rows, several splits of the prefix, partial tiles
     # of both; some sequences shorter than the prefix, one empty
