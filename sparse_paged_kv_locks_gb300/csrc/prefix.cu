@@ -191,10 +191,6 @@ __device__ __forceinline__ void tm_st16(uint32_t addr,
       "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// shared-memory writes of this thread, seen by the tensor core
-__device__ __forceinline__ void fence_to_async() {
-  asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-}
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(
                    smem_u32(bar))

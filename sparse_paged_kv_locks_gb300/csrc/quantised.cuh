@@ -124,6 +124,15 @@ struct PageLists {
   }
 };
 
+// This thread's accesses to shared memory so far come before what the copy
+// engine and the tensor core do there for it later: reads of a buffer before
+// the next copy into it (without the fence, a loop that had only __syncwarp
+// between them was seen to read the next tile's values), writes before the
+// product that reads them.
+__device__ __forceinline__ void fence_to_async() {
+  asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+}
+
 __device__ __forceinline__ int checked_len(const int32_t *seq_lens, int b,
                                            int max_pages, int32_t *status) {
   const int L = __ldg(seq_lens + b);
