@@ -561,19 +561,19 @@ locks_status_t locks_quantised_decode(
 
 // the partials of the shared pages
 struct PrefixRegion {
-  int splits;
+  PrefixPlan plan;
   float *o_part;
   float2 *ml_part;
   size_t bytes;
 };
 static PrefixRegion prefix_region(uint8_t *at, int batch, int h_q, int h_kv,
                                   int pages) {
-  if (pages == 0 || batch == 0) return {0, nullptr, nullptr, 0};
-  const int splits = prefix_splits(batch, h_kv, h_q / h_kv, pages);
-  if (splits == 0) return {0, nullptr, nullptr, 0};
-  const size_t rows = (size_t)splits * batch * h_q;
+  if (pages == 0 || batch == 0) return {{0, false}, nullptr, nullptr, 0};
+  const PrefixPlan plan = prefix_plan(batch, h_kv, h_q / h_kv, pages);
+  if (plan.splits == 0) return {plan, nullptr, nullptr, 0};
+  const size_t rows = (size_t)plan.splits * batch * h_q;
   const size_t sums = round_up(rows * kDim * 4, 256);
-  return {splits, reinterpret_cast<float *>(at),
+  return {plan, reinterpret_cast<float *>(at),
           reinterpret_cast<float2 *>(at + sums),
           sums + round_up(rows * 8, 256)};
 }
@@ -615,9 +615,9 @@ locks_status_t locks_prefix_decode(
   const int G = h_q / h_kv;
   int32_t *status = reinterpret_cast<int32_t *>(ws);
   cudaError_t e = cudaSuccess;
-  if (p.splits > 0)
+  if (p.plan.splits > 0)
     e = launch_prefix(q, records, num_phys_pages, prefix_table, prefix_pages,
-                      batch, h_kv, G, p.splits, p.o_part, p.ml_part, status,
+                      batch, h_kv, G, p.plan, p.o_part, p.ml_part, status,
                       (cudaStream_t)stream);
   if (e == cudaSuccess)
     e = launch_qdecode(q, records, num_phys_pages, page_table, seq_lens,
@@ -625,7 +625,7 @@ locks_status_t locks_prefix_decode(
                        prefix_pages,
                        (int)decode_warps_cap(batch, h_kv, max_pages), o_out,
                        lse_out, r.o_part, r.ml_part, r.meta, p.o_part,
-                       p.ml_part, p.splits, status, (cudaStream_t)stream);
+                       p.ml_part, p.plan.splits, status, (cudaStream_t)stream);
   return e == cudaSuccess ? LOCKS_OK : fail_cuda(e);
 }
 

@@ -194,11 +194,16 @@ cudaError_t launch_qdecode(const void *q, const void *records,
 int qdecode_max_batch();
 
 // attention of all query rows over the shared pages, in `splits` partials
-// (prefix.cu; 0: not worth a kernel of its own)
-int prefix_splits(int batch, int h_kv, int G, int pages);
+// (prefix.cu; 0: not worth a kernel of its own), a CTA taking two tiles of
+// query rows if `wide`
+struct PrefixPlan {
+  int splits;
+  bool wide;
+};
+PrefixPlan prefix_plan(int batch, int h_kv, int G, int pages);
 cudaError_t launch_prefix(const void *q, const void *records,
                           int64_t num_phys, const int32_t *table, int pages,
-                          int batch, int h_kv, int G, int splits,
+                          int batch, int h_kv, int G, PrefixPlan plan,
                           float *o_part, float2 *ml_part, int32_t *status,
                           cudaStream_t stream);
 

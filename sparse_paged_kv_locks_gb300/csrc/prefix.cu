@@ -3,10 +3,10 @@
 // (the mathematics and the partials are those of the single-token kernel,
 // qdecode.cu; the sequences' own pages and the merge are its work).
 //
-// A CTA takes 128 query rows of a KV head and a range of 128-token tiles.
-// Both products are tcgen05 matrix products with fp32 accumulators in tensor
-// memory: S = Q K^T, O += W V with the weights W in fp16 in tensor memory
-// over the scores they came from.
+// A CTA takes one or two tiles of 128 query rows of a KV head and a range of
+// 128-token tiles.  Both products are tcgen05 matrix products with fp32
+// accumulators in tensor memory: S = Q K^T, O += W V with the weights W in
+// fp16 in tensor memory over the scores they came from.
 //
 // Keys take part as they are stored: the e4m3 rows are copied to shared
 // memory, and the query row is the sum of two e4m3 rows, hi + lo, after a
@@ -22,52 +22,64 @@
 // tensor core's operand by s & 7.  The two agree on even rows; an odd row's
 // halves trade places in shared memory before its product.
 //
-// Eight warps: 0-3 softmax, a query row to a thread, so that maxima and sums
-// need no exchange; 4 issues the products and has the values (with all
-// scales) copied; 5 has the keys copied and mends them; 6 and 7 widen the
-// values.  A buffer's next copy starts when it has been read: the keys of
-// tile j + 1 come and its values are read to registers while the softmax of
-// tile j runs.  Two CTAs fit an SM, with their columns of tensor memory fill
-// it, and one's softmax runs under the other's products.
+// Four warps per row tile do its softmax, a query row to a thread, so that
+// maxima and sums need no exchange; one warp issues the products; one has the
+// keys copied and mends them; two have the values (with all scales) copied,
+// and widen them, four pages of a tile each.  With one row tile two CTAs fit an
+// SM, with their columns of tensor memory fill it, and one's softmax runs under
+// the other's products; a buffer's next copy starts when it has been read.
+// With two row tiles a CTA has an SM to itself, two buffers of everything, and
+// its keys and values serve both tiles, whose softmax and products take turns.
 //
-// Bound: for many rows, the chain scores -> softmax -> weights -> products of a
-// tile, about 4,800 cycles with another CTA's beside it (softmax 2,600, the
-// two products 1,100, the rest waits between the roles); tensor cores, special
-// functions and shared memory are each below two thirds.  With the softmax
-// left out a 128K prefix for 64 sequences and 64 query heads took 230 us, with
-// the products as well 205, against 303; without the exponentials 290.  For
-// few rows, the bytes of the records.  What was slower on that prefix: loads
-// to registers instead of bulk copies (the pages lie far apart, and the proxy
-// fence before a product waits for its thread's loads; 610 us), copies of
-// single rows to their swizzled places (850 us), three warps that each do a
-// third of everything (348 us), tiles of 64 tokens with two or three buffers
-// of everything (335 us: a product then reads the query from shared memory for
-// half as many columns), two threads to a row in eight softmax warps of 96
-// registers (347 us), the scores of the next tile's first half under the
-// softmax of this one's second (two buffers of keys, products of 64 columns;
-// 323 us: every role then ran slower beside the others).
+// Bound: for many rows, the chain scores -> softmax -> weights -> products of
+// a tile: some 2,150 cycles of softmax and as many from its weights to its next
+// scores, in which the tensor core is busy with both row tiles for about 2,650
+// of 4,300.  The product of keys and query reads shared memory at 122 bytes a
+// cycle of 128 and runs at 70% of its rate.  A 128K prefix for 64 sequences and
+// 64 query heads takes 276 us in this form (300 with one row tile to a CTA);
+// with half of that product left out 24 us less, of the other 18, without the
+// exponentials 18, without the loads of key scales 19; without the stores of
+// widened values or of mended keys the same.  For few rows, the start and end
+// of a CTA and the bytes of the records.
+//
+// What was slower on that prefix, with two row tiles: the products of a tile's
+// first half under the softmax of its second (307 us), the second half's
+// scores loaded under the first half's exponentials (285 us), key scales in
+// bf16 (283 us); three buffers of keys took as long as two.  With one row tile
+// (then 303 us): loads to registers instead of bulk copies (the pages lie far
+// apart, and the proxy fence before a product waits for its thread's loads;
+// 610 us), copies of single rows to their swizzled places (850 us), three warps
+// that each do a third of everything (348 us), tiles of 64 tokens with two or
+// three buffers of everything (335 us: a product then reads the query from
+// shared memory for half as many columns), two threads to a row in eight
+// softmax warps of 96 registers (347 us), the scores of the next tile's first
+// half under the softmax of this one's second (323 us).
 #include "launch.h"
 #include "quantised.cuh"
 
 namespace locks {
 
-constexpr int kPfRows = 128;   // query rows of a CTA
+constexpr int kPfRows = 128;   // query rows of a row tile
 constexpr int kPfTile = 128;   // tokens of a tile
 constexpr int kPfPages = kPfTile / kPage;
-constexpr int kPfThreads = 256;
 constexpr int kPfWiden = 2;    // warps that widen values
+constexpr int kPfOwn = kPfPages / kPfWiden;  // pages of each of them
 constexpr int kPfQuery = kPfRows * kDim;    // hi or lo of the query, 16 KB
 constexpr int kPfCodes = kPfTile * kDim;    // a tile of e4m3 keys, 16 KB
 constexpr int kPfBlock = kPfTile * 128;     // 64 dims of fp16 values, 16 KB
 constexpr int kPfRest = kQRec - kQOffV;     // values and scales of a record
 constexpr int kPfRaw = kPfPages * kPfRest;  // a tile of them
-constexpr int kPfSmem =
-    2 * kPfQuery + kPfCodes + 2 * kPfBlock + kPfRaw + 1024;
+// per row tile of a CTA: its query, and one more buffer of all the rest
+constexpr int kPfPart = 2 * kPfQuery + kPfCodes + 2 * kPfBlock + kPfRaw;
 constexpr int kPfColumns = 256;             // tensor memory: S, then O
 constexpr int kPfColO = kPfTile;
+template <int R>
+constexpr int kPfThreads = 32 * (4 * R + 2 + kPfWiden);
+template <int R>
+constexpr int kPfSmem = R * kPfPart + 1024;
 constexpr float kPfScale = 0.12751743074602467f;  // log2(e) / sqrt(128)
 // fewest (sequence, KV head, page) triples that are worth the kernel
-constexpr long long kPfMinShared = 24576;
+constexpr long long kPfMinShared = 12288;
 constexpr float kPfLift = 8.f;   // as in the single-token kernel
 constexpr float kPfSlack = 7.f;
 
@@ -265,16 +277,19 @@ struct PfArgs {
   int32_t *status;
 };
 
+template <int R>
 struct PfShared {
   // of tile j, at j & 1: scales of the keys, E and 2^-E of the pages' values,
-  // and which pages are there
+  // and which pages are there (a widening warp's each)
   float k_scale[2][kPfTile];
   float v_exp[2][kPfPages], v_inv[2][kPfPages];
-  uint32_t there[2];
+  uint32_t there[2][kPfWiden];
   uint32_t tmem;
   int dead;
-  uint64_t q_full, k_raw, k_full, v_raw, v_read, v_full, info[2];
-  uint64_t p_full, qk_done, pv_done, drain;
+  uint64_t q_full[R], qk_done[R], p_full[R], o_done[R];      // of a row tile
+  uint64_t k_raw[R], k_full[R], k_free[R];                   // of a buffer
+  uint64_t v_raw[kPfWiden][R], v_full[R], v_free[R];
+  uint64_t info[2], drain;
 };
 
 // one lane of the warp, for what a warp does once
@@ -288,7 +303,8 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // false when the wait gave up, or some other thread's did
-__device__ __forceinline__ bool pf_wait(PfShared &sh, uint64_t *bar,
+template <int R>
+__device__ __forceinline__ bool pf_wait(PfShared<R> &sh, uint64_t *bar,
                                         uint32_t phase) {
   if (mbar_try_wait(bar, phase)) return true;
   const long long t0 = clock64();
@@ -302,50 +318,63 @@ __device__ __forceinline__ bool pf_wait(PfShared &sh, uint64_t *bar,
   return false;
 }
 
-__global__ void __launch_bounds__(kPfThreads, 2)
+// tile j's use of a ring of R
+template <int R>
+__device__ __forceinline__ bool pf_wait_ring(PfShared<R> &sh,
+                                             uint64_t (&bars)[R], int j) {
+  return pf_wait(sh, bars + j % R, j / R & 1);
+}
+
+template <int R>
+__global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
     prefix_kernel(const PfArgs a) {
   extern __shared__ uint8_t raw_smem[];
-  __shared__ PfShared sh;
+  __shared__ PfShared<R> sh;
   // the same for all of a warp, and known to be: products and copies take
   // their operands from uniform registers
   const int tid = threadIdx.x, lane = tid & 31;
   const int wid = __shfl_sync(0xffffffffu, tid >> 5, 0);
   // swizzled tiles start at multiples of 1024 bytes
   const uint32_t q_s = (smem_u32(raw_smem) + 1023u) & ~1023u;
-  const uint32_t k_s = q_s + 2 * kPfQuery;
-  const uint32_t v_s = k_s + kPfCodes;
-  const uint32_t raw_s = v_s + 2 * kPfBlock;  // [page][kPfRest]
+  const uint32_t k_s = q_s + R * 2 * kPfQuery;
+  const uint32_t v_s = k_s + R * kPfCodes;
+  const uint32_t raw_s = v_s + R * 2 * kPfBlock;  // [buffer][page][kPfRest]
+  constexpr int kProducts = 4 * R, kKeys = kProducts + 1;  // warps
 
-  // this CTA's KV head, query rows and tiles
+  // this CTA's KV head, row tiles and tiles
   const int tiles = (a.pages + kPfPages - 1) / kPfPages;
-  const int rt = blockIdx.x % a.row_tiles;
-  const int rest = blockIdx.x / a.row_tiles;
+  const int rts = (a.row_tiles + R - 1) / R;
+  const int rt = blockIdx.x % rts * R;
+  const int rest = blockIdx.x / rts;
   const int h = rest % a.h_kv, split = rest / a.h_kv;
   const int t0 = (int)((long long)split * tiles / a.splits);
   const int t1 = (int)((long long)(split + 1) * tiles / a.splits);
   const int n = t1 - t0;
+  const int nt = min(R, a.row_tiles - rt);
   const int rows = a.batch * a.G;
-  const int row = rt * kPfRows + tid;  // softmax warps
 
-  if (wid == 4) {
+  if (wid == kProducts) {
     asm volatile(
         "tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n"
         " tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::"r"(
             smem_u32(&sh.tmem)),
-        "r"(kPfColumns)
+        "r"(R * kPfColumns)
         : "memory");
     if (lane == 0) {
-      mbar_init(&sh.q_full, 4);
-      mbar_init(&sh.k_raw, 1);
-      mbar_init(&sh.k_full, 1);
-      mbar_init(&sh.v_raw, 1);
-      mbar_init(&sh.v_read, kPfWiden + 1);
-      mbar_init(&sh.v_full, kPfWiden);
-      mbar_init(sh.info, kPfWiden + 1);
-      mbar_init(sh.info + 1, kPfWiden + 1);
-      mbar_init(&sh.p_full, 4);
-      mbar_init(&sh.qk_done, 1);
-      mbar_init(&sh.pv_done, 1);
+      for (int i = 0; i < R; ++i) {
+        mbar_init(sh.q_full + i, 4);
+        mbar_init(sh.qk_done + i, 1);
+        mbar_init(sh.p_full + i, 4);
+        mbar_init(sh.o_done + i, 1);
+        mbar_init(sh.k_raw + i, 1);
+        mbar_init(sh.k_full + i, 1);
+        mbar_init(sh.k_free + i, 1);
+        for (int w = 0; w < kPfWiden; ++w) mbar_init(sh.v_raw[w] + i, 1);
+        mbar_init(sh.v_full + i, kPfWiden);
+        mbar_init(sh.v_free + i, 1);
+      }
+      mbar_init(sh.info, kPfWiden);
+      mbar_init(sh.info + 1, kPfWiden);
       mbar_init(&sh.drain, 1);
       sh.dead = 0;
       fence_mbar_init();
@@ -358,7 +387,11 @@ __global__ void __launch_bounds__(kPfThreads, 2)
   pdl_wait();
   pdl_trigger();
 
-  if (wid < 4) {
+  const int tile = wid >> 2;  // row tile of a softmax warp
+  if (wid < kProducts && tile >= nt) {
+    // no rows
+  } else if (wid < kProducts) {
+    const int row = rt * kPfRows + tid;
     // the query rows: hi and lo codes, the scale that they leave to scores
     const uint4 *src = reinterpret_cast<const uint4 *>(
         a.q + ((size_t)(row / a.G) * a.h_kv * a.G + (size_t)h * a.G +
@@ -404,27 +437,28 @@ __global__ void __launch_bounds__(kPfThreads, 2)
                            e4m3x2_from(a2 - h1.x, a3 - h1.y) << 16;
         }
       }
-      const uint32_t at = q_s + tid * 128 + ((i ^ (tid & 7)) << 4);
+      const uint32_t at = q_s + tile * 2 * kPfQuery + (tid & 127) * 128 +
+                          ((i ^ (tid & 7)) << 4);
       st_shared_v4(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
       st_shared_v4(at + kPfQuery, make_uint4(lo[0], lo[1], lo[2], lo[3]));
     }
     fence_to_async();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.q_full);
+    if (lane == 0) mbar_arrive(sh.q_full + tile);
     // ------------------------------------------------------------- softmax
-    const uint32_t mine = tm + ((uint32_t)(wid * 32) << 16);
+    const uint32_t mine =
+        tm + tile * kPfColumns + ((uint32_t)((wid & 3) * 32) << 16);
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       const int par = j & 1;
-      // all products before S(j), among them O(j - 1), are done
+      // with S(j) all products before it, among them O(j - 1), are done
       ok = pf_wait(sh, sh.info + par, j >> 1 & 1) &&
-           pf_wait(sh, &sh.qk_done, j & 1) &&
-           (j == 0 || pf_wait(sh, &sh.pv_done, (j - 1) & 1));
+           pf_wait(sh, sh.qk_done + tile, j & 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tm_fence_after();
-      const uint32_t there = sh.there[par];
+      const uint32_t there = sh.there[par][0] | sh.there[par][1];
       // 64 columns at a time: their weights go over the scores they come
       // from, in columns that have been read
       for (int c = 0; c < 2; ++c) {
@@ -515,9 +549,9 @@ __global__ void __launch_bounds__(kPfThreads, 2)
       tm_wait_st();
       tm_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.p_full);
+      if (lane == 0) mbar_arrive(sh.p_full + tile);
     }
-    if (ok) ok = pf_wait(sh, &sh.pv_done, (n - 1) & 1);
+    if (ok) ok = pf_wait(sh, sh.o_done + tile, 0);
     ok = __all_sync(0xffffffffu, ok);
     tm_fence_after();
     // partials: 16 rows at a time as matrix fragments (row lane / 4 and + 8,
@@ -529,7 +563,7 @@ __global__ void __launch_bounds__(kPfThreads, 2)
     };
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      const int r0 = rt * kPfRows + 32 * wid + 16 * half + (lane >> 2);
+      const int r0 = row - lane + 16 * half + (lane >> 2);
       float *d0 = a.o_part + place(r0) * kDim + 2 * (lane & 3);
       float *d1 = a.o_part + place(r0 + 8) * kDim + 2 * (lane & 3);
 #pragma unroll
@@ -551,101 +585,104 @@ __global__ void __launch_bounds__(kPfThreads, 2)
     if (row < rows) a.ml_part[place(row)] = make_float2(m, ok ? l : 0.f);
   } else {
     auto good = [&](int ph) -> bool { return ph >= 0 && ph < a.num_phys; };
-    // page lane & 7 of tile t as the table has it, -1 past the end
-    auto page = [&](int t) -> int {
-      const int pg = t * kPfPages + (lane & (kPfPages - 1));
-      return t < t1 && pg < a.pages ? __ldg(a.table + pg) : -1;
+    // page `pg` of tile j as the table has it, -1 past the end
+    auto page = [&](int j, int pg) -> int {
+      pg += (t0 + j) * kPfPages;
+      return j < n && pg < a.pages ? __ldg(a.table + pg) : -1;
     };
-    auto pages_there = [&](int ph) -> uint32_t {
-      return __ballot_sync(0xffffffffu, good(ph)) & ((1u << kPfPages) - 1);
-    };
-    // keys, or values and scales, of a tile's pages (ph: page lane & 7); one
-    // arrival for all, a lane to a page
-    auto copy = [&](int ph, int off, uint32_t bytes, uint32_t to,
-                    uint64_t *bar) {
-      const uint32_t there = pages_there(ph);
+    // a part of the records of `pages` pages (ph: page of the lane); one
+    // arrival for all, a lane to a page; which were there
+    auto copy = [&](int ph, int pages, int off, uint32_t bytes, uint32_t to,
+                    uint64_t *bar) -> uint32_t {
+      const bool here = lane < pages && good(ph);
+      const uint32_t there = __ballot_sync(0xffffffffu, here);
       if (lane == 0) mbar_arrive_tx(bar, __popc(there) * bytes);
       __syncwarp();
-      if (lane < kPfPages && (there >> lane & 1))
+      if (here)
         bulk_rows(to + lane * bytes,
                   a.records + ((size_t)ph * a.h_kv + h) * kQRec + off, bytes,
                   bar);
       __syncwarp();
+      return there;
     };
-    // pages of tiles j, j + 1
-    int ph = page(t0), ph_next = page(t0 + 1);
     bool ok = true;
-    if (wid == 4) {
-      // ------------------------------------------------ products, values
-      int copied = 0;  // tiles
-      auto copy_values = [&](int ph) {
-        ++copied;
-        // a page that is not there reads as zeros (written before the
-        // arrival that the readers wait for)
-        for (uint32_t gone = ~pages_there(ph) & ((1u << kPfPages) - 1); gone;
-             gone &= gone - 1)
-          for (int i = lane; i < kPfRest / 16; i += 32)
-            st_shared_v4(raw_s + (__ffs(gone) - 1) * kPfRest + 16 * i,
-                         make_uint4(0u, 0u, 0u, 0u));
-        __syncwarp();
-        copy(ph, kQOffV, kPfRest, raw_s, &sh.v_raw);
-      };
+    if (wid == kProducts) {
+      // -------------------------------------------------------- products
       const uint64_t dq = mat_desc(q_s, 16), dk = mat_desc(k_s, 16);
       const uint64_t dv = mat_desc(v_s, kPfBlock);
-      copy_values(ph);
-      for (int j = 0; j < n; ++j) {
-        ok = (j > 0 || pf_wait(sh, &sh.q_full, 0)) &&
-             pf_wait(sh, &sh.k_full, j & 1);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        tm_fence_after();
+      // S(j) of row tile t, and after the last one its keys may go
+      auto scores = [&](int t, int j) {
         if (elect_one()) {
+          const uint64_t q = dq + t * (2 * kPfQuery >> 4);
+          const uint64_t k = dk + j % R * (kPfCodes >> 4);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)  // hi, then lo
-            mma_ss(tm, dq + ((kk >> 2) * (kPfQuery >> 4) + (kk & 3) * 2),
-                   dk + (kk & 3) * 2, kPfDescS, kk > 0);
-          mma_commit(&sh.qk_done);
+            mma_ss(tm + t * kPfColumns,
+                   q + ((kk >> 2) * (kPfQuery >> 4) + (kk & 3) * 2),
+                   k + (kk & 3) * 2, kPfDescS, kk > 0);
+          mma_commit(sh.qk_done + t);
+          if (t == nt - 1) mma_commit(sh.k_free + j % R);
         }
         __syncwarp();
-        if (j + 1 < n) {
-          ok = pf_wait(sh, &sh.v_read, j & 1);
-          if (!__all_sync(0xffffffffu, ok)) break;
-          copy_values(ph_next);
-          ph_next = page(t0 + j + 2);
-        }
-        ok = pf_wait(sh, &sh.v_full, j & 1) && pf_wait(sh, &sh.p_full, j & 1);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        tm_fence_after();
+      };
+      auto weighted = [&](int t, int j) {
         if (elect_one()) {
+          const uint64_t v = dv + j % R * (2 * kPfBlock >> 4);
+          const uint32_t at = tm + t * kPfColumns;
 #pragma unroll
           for (int kk = 0; kk < kPfTile / 16; ++kk)
-            mma_ts(tm + kPfColO, tm + 8 * kk, dv + kk * (kPage * 128 >> 4),
+            mma_ts(at + kPfColO, at + 8 * kk, v + kk * (kPage * 128 >> 4),
                    kPfDescO, j > 0 || kk > 0);
-          mma_commit(&sh.pv_done);
+          if (t == nt - 1) mma_commit(sh.v_free + j % R);
+          if (j == n - 1) mma_commit(sh.o_done + t);
         }
         __syncwarp();
-      }
+      };
+      for (int j = -1; j < n && ok; ++j)
+        for (int t = 0; t < nt; ++t) {
+          if (j >= 0) {
+            ok = (t > 0 || pf_wait_ring(sh, sh.v_full, j)) &&
+                 pf_wait(sh, sh.p_full + t, j & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tm_fence_after();
+            weighted(t, j);
+          }
+          if (j + 1 < n) {
+            ok = (t > 0 || pf_wait_ring(sh, sh.k_full, j + 1)) &&
+                 (j >= 0 || pf_wait(sh, sh.q_full + t, 0));
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tm_fence_after();
+            scores(t, j + 1);
+          }
+        }
       if (*(volatile int *)&sh.dead && elect_one()) {
         // give what is in flight a last, bounded chance to finish
         set_status(a.status, LOCKS_DEV_TIMEOUT);
         mma_commit(&sh.drain);
         q_wait(&sh.drain, 0);
-        q_wait(&sh.v_raw, (copied - 1) & 1);
       }
-    } else if (wid == 5) {
+    } else if (wid == kKeys) {
       // ------------------------------------------------------------ keys
       int copied = 0;  // tiles
-      auto copy_keys = [&](int j, int ph) {
-        ++copied;
+      auto copy_keys = [&](int ph) {
+        const int j = copied++;
         if (lane < kPfPages && !good(ph) &&
             (t0 + j) * kPfPages + lane < a.pages)
           set_status(a.status, LOCKS_DEV_BAD_PAGE_ID);
-        copy(ph, 0, kQCodes, k_s, &sh.k_raw);
+        copy(ph, kPfPages, 0, kQCodes, k_s + j % R * kPfCodes,
+             sh.k_raw + j % R);
       };
-      // the halves of odd key rows trade places
-      auto mend_keys = [&]() {
+      for (int j = 0; j < R && j < n; ++j) copy_keys(page(j, lane));
+      int ph = page(R, lane);
+      for (int j = 0; j < n; ++j) {
+        ok = pf_wait_ring(sh, sh.k_raw, j);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        // the halves of odd key rows trade places
 #pragma unroll
         for (int h2 = 0; h2 < 2; ++h2) {
-          const uint32_t at = k_s + h2 * 4 * kQCodes +
+          const uint32_t at = k_s + j % R * kPfCodes + h2 * 4 * kQCodes +
                               (2 * (lane >> 2) + 1) * 128 + 16 * (lane & 3);
           // rows that are read together start with different halves
           const uint32_t a0 = at + (lane & 4 ? 64 : 0);
@@ -664,76 +701,94 @@ __global__ void __launch_bounds__(kPfThreads, 2)
         }
         fence_to_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.k_full);
-      };
-      copy_keys(0, ph);
-      ok = pf_wait(sh, &sh.k_raw, 0);
-      ok = __all_sync(0xffffffffu, ok);
-      if (ok) mend_keys();
-      for (int j = 0; j < n && ok; ++j) {
-        // what softmax needs to know of tile j (S(j - 1) is done, so O(j - 2)
-        // is, and the softmax that was told of j - 2)
-        ok = pf_wait(sh, &sh.v_raw, j & 1);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        const uint32_t there = pages_there(ph);
-#pragma unroll
-        for (int i = 0; i < kPfPages / 2; ++i) {
-          const int pg = 2 * i + (lane >> 4), sl = lane & 15;
-          uint32_t e;
-          asm volatile("ld.shared.u8 %0, [%1];\n"
-                       : "=r"(e)
-                       : "r"(raw_s + pg * kPfRest + (kQOffKE - kQOffV) + sl));
-          sh.k_scale[j & 1][kPage * pg + sl] = __uint_as_float(e << 23);
-        }
-        if (lane == 0) sh.there[j & 1] = there;
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(sh.info + (j & 1));
-          mbar_arrive(&sh.v_read);
-        }
-        ph = ph_next;
-        if (j + 1 < n) {  // S(j) done: its keys may go
-          ok = pf_wait(sh, &sh.qk_done, j & 1);
+        if (lane == 0) mbar_arrive(sh.k_full + j % R);
+        if (copied < n && copied == j + 1) {
+          // the scores of the tile before in this buffer done: it may go
+          ok = pf_wait_ring(sh, sh.k_free, copied - R);
           if (!__all_sync(0xffffffffu, ok)) break;
-          copy_keys(j + 1, ph);
-          ph_next = page(t0 + j + 2);
-          ok = pf_wait(sh, &sh.k_raw, (j + 1) & 1);
-          if (!__all_sync(0xffffffffu, ok)) break;
-          mend_keys();
+          copy_keys(ph);
+          ph = page(copied, lane);
         }
       }
-      if (*(volatile int *)&sh.dead) q_wait(&sh.k_raw, (copied - 1) & 1);
+      if (*(volatile int *)&sh.dead)
+        for (int j = max(0, copied - R); j < copied; ++j)
+          q_wait(sh.k_raw + j % R, j / R & 1);
     } else {
       // ---------------------------------------------------------- values
-      // A warp takes four pages of a tile, four slots at a time.  Eight
-      // lanes that read and store a 16-byte group each have the same half of
-      // the dims of slots s and s + 1, which either swizzle keeps in
-      // different banks.
-      const int first = 4 * (wid - 6);
+      // A warp takes kPfOwn pages of a tile, four slots at a time, and has
+      // them copied itself.  Eight lanes that read and store a 16-byte group
+      // each have the same half of the dims of slots s and s + 1, which
+      // either swizzle keeps in different banks.
+      const int own = wid - kKeys - 1, first = own * kPfOwn;
       const int s4 = (lane >> 4) * 2 + (lane >> 2 & 1);
       const int c = (lane & 3) | (lane >> 1 & 4);
-      for (int j = 0; j < n; ++j) {
-        ok = pf_wait(sh, &sh.v_raw, j & 1);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        uint4 raw[16];
+      const uint32_t mine = raw_s + first * kPfRest;
+      int copied = 0;  // tiles
+      auto copy_values = [&](int ph) -> uint32_t {
+        const int b = copied++ % R;
+        const uint32_t to = mine + b * kPfRaw;
+        const uint32_t there =
+            copy(ph, kPfOwn, kQOffV, kPfRest, to, sh.v_raw[own] + b);
+        // a page that is not there reads as zeros
+        for (uint32_t gone = ~there & ((1u << kPfOwn) - 1); gone;
+             gone &= gone - 1)
+          for (int i = lane; i < kPfRest / 16; i += 32)
+            st_shared_v4(to + (__ffs(gone) - 1) * kPfRest + 16 * i,
+                         make_uint4(0u, 0u, 0u, 0u));
+        __syncwarp();
+        return there;
+      };
+      uint32_t there[R];  // of tiles j to j + R - 1
 #pragma unroll
-        for (int u = 0; u < 16; ++u) {
+      for (int j = 0; j < R; ++j)
+        there[j] = j < n ? copy_values(page(j, first + lane)) : 0u;
+      int ph = page(R, first + lane);
+      for (int j = 0; j < n; ++j) {
+        ok = pf_wait_ring(sh, sh.v_raw[own], j);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        const uint32_t from = mine + j % R * kPfRaw;
+        uint4 raw[4 * kPfOwn];
+#pragma unroll
+        for (int u = 0; u < 4 * kPfOwn; ++u) {
           const int sl = 4 * (u & 3) + s4;
-          raw[u] = lds128(raw_s + (first + (u >> 2)) * kPfRest + sl * kDim +
+          raw[u] = lds128(from + (u >> 2) * kPfRest + sl * kDim +
                           16 * q_group(c, sl));
         }
-        // lane 16 i + slot: scales of rows of pages i and 2 + i; factor:
-        // 2^(e - E), exact down to 2^-24 and zero below
-        uint32_t factor[2];
+        // lane 16 i + slot: exponents of rows of pages i and 2 + i
+        uint32_t ke[kPfOwn / 2], ve[kPfOwn / 2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int pg = first + 2 * i + (lane >> 4);
-          uint32_t e;
+        for (int i = 0; i < kPfOwn / 2; ++i) {
+          const uint32_t at = from + (2 * i + (lane >> 4)) * kPfRest + (lane & 15);
           asm volatile("ld.shared.u8 %0, [%1];\n"
-                       : "=r"(e)
-                       : "r"(raw_s + pg * kPfRest + (kQOffVE - kQOffV) +
-                             (lane & 15)));
-          uint32_t top = e;
+                       : "=r"(ke[i])
+                       : "r"(at + (kQOffKE - kQOffV)));
+          asm volatile("ld.shared.u8 %0, [%1];\n"
+                       : "=r"(ve[i])
+                       : "r"(at + (kQOffVE - kQOffV)));
+        }
+        // all has been read before the next copy is written there
+        fence_to_async();
+        __syncwarp();
+        const uint32_t now = there[0];
+        if (copied < n) {
+          if (R > 1) there[0] = there[R - 1];
+          there[R - 1] = copy_values(ph);
+          ph = page(copied, first + lane);
+        } else if (R > 1) {
+          there[0] = there[R - 1];
+        }
+        // what softmax needs to know of the tile, in the place of j - 2's:
+        // O(j - 2) is done
+        if (R == 2 && j >= 2) {
+          ok = pf_wait_ring(sh, sh.v_free, j - R);
+          if (!__all_sync(0xffffffffu, ok)) break;
+        }
+        // factor: 2^(e - E), exact down to 2^-24 and zero below
+        uint32_t factor[kPfOwn / 2];
+#pragma unroll
+        for (int i = 0; i < kPfOwn / 2; ++i) {
+          const int pg = first + 2 * i + (lane >> 4);
+          uint32_t top = ve[i];
 #pragma unroll
           for (int o = 1; o < 16; o <<= 1)
             top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -741,19 +796,22 @@ __global__ void __launch_bounds__(kPfThreads, 2)
             sh.v_exp[j & 1][pg] = (float)((int)top - 127);
             sh.v_inv[j & 1][pg] = exp2_int(127 - (int)top);
           }
+          sh.k_scale[j & 1][kPage * pg + (lane & 15)] =
+              __uint_as_float(ke[i] << 23);
           factor[i] = h2_as_u32(
-              __float2half2_rn(exp2_int(max(-126, (int)e - (int)top))));
+              __float2half2_rn(exp2_int(max(-126, (int)ve[i] - (int)top))));
         }
+        if (lane == 0) sh.there[j & 1][own] = now << first;
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(sh.info + (j & 1));
-          mbar_arrive(&sh.v_read);
-        }
+        if (lane == 0) mbar_arrive(sh.info + (j & 1));
         // O(j - 1) done: its values may go
-        ok = j == 0 || pf_wait(sh, &sh.pv_done, (j - 1) & 1);
-        if (!__all_sync(0xffffffffu, ok)) break;
+        if (R == 1 && j >= 1) {
+          ok = pf_wait_ring(sh, sh.v_free, j - R);
+          if (!__all_sync(0xffffffffu, ok)) break;
+        }
+        const uint32_t to = v_s + j % R * 2 * kPfBlock;
 #pragma unroll
-        for (int u = 0; u < 16; ++u) {
+        for (int u = 0; u < 4 * kPfOwn; ++u) {
           const int sl = 4 * (u & 3) + s4;
           const __half2 x = u32_as_h2(__shfl_sync(
               0xffffffffu, factor[u >> 3], 16 * (u >> 2 & 1) + sl));
@@ -765,85 +823,111 @@ __global__ void __launch_bounds__(kPfThreads, 2)
             y[2 * k + 1] = h2_as_u32(__hmul2(u32_as_h2(e4m3x2_hi(w[k])), x));
           }
           const int r = (first + (u >> 2)) * kPage + sl;
-          st_shared_v4(v_s + tile_at(r, 2 * c),
+          st_shared_v4(to + tile_at(r, 2 * c),
                        make_uint4(y[0], y[1], y[2], y[3]));
-          st_shared_v4(v_s + tile_at(r, 2 * c + 1),
+          st_shared_v4(to + tile_at(r, 2 * c + 1),
                        make_uint4(y[4], y[5], y[6], y[7]));
         }
         fence_to_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.v_full);
+        if (lane == 0) mbar_arrive(sh.v_full + j % R);
       }
+      if (*(volatile int *)&sh.dead)
+        for (int j = max(0, copied - R); j < copied; ++j)
+          q_wait(sh.v_raw[own] + j % R, j / R & 1);
     }
   }
   __syncwarp();
   tm_fence_before();
   __syncthreads();
-  if (wid == 4)
+  if (wid == kProducts)
     asm volatile(
         "tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tm),
-        "r"(kPfColumns)
+        "r"(R * kPfColumns)
         : "memory");
 }
 
 // ---------------------------------------------------------------------------
 // launcher
 // ---------------------------------------------------------------------------
-// How many ranges the prefix's tiles are cut into: enough CTAs for two to an
-// SM, and no more waves of them than pay.  A tile costs a CTA about 2.6 us
-// with another beside it, its start and end 8 us, a row's partial 1 KB of
-// traffic.  A rule on sizes alone (152 SMs), so that the workspace's size
+// How many ranges the prefix's tiles are cut into, and whether a CTA takes two
+// row tiles.  A rule on sizes alone (152 SMs), so that the workspace's size
 // needs no GPU.
 //
-// 0: too little to share, every sequence reads the pages itself.  (Sequences,
-// KV heads, pages, G = 4 unless given: read by each against once.)  8, 8, 128:
-// 13.5 and 23 us; 8, 8, 512: 30.5 and 26; 2, 8, 1024: 24.6 and 24.4; 2, 8,
-// 4096: 49 and 47; 32, 8, 32: 12.3 and 24.5; 32, 8, 128: 31 and 26; 64, 8, 32,
-// G = 8: 21 and 37; 16, 8, 256, G = 16: 41 and 30; 256, 8, 12, G = 1: 31.5 and
-// 26; 128, 1, 512, G = 8: 46 and 28; one sequence, 8, 8192: 64 and 77.  A long
-// prefix of one KV head (4, 1, 8192, G = 16: 48 and 34) takes all 304 ranges;
-// with 64 at most it took 43.
-int prefix_splits(int batch, int h_kv, int G, int pages) {
-  if (batch < 2 || (long long)batch * h_kv * pages < kPfMinShared) return 0;
-  const long long slots = 304;
+// The estimate (us) that picks among them: a tile of a CTA 1.6 alone on its
+// SM, 2.4 with another beside it, 2.0 of two row tiles; 6 for a CTA's start
+// and end, a row's partial 1 KB of traffic; and the sequences' own pages,
+// whose kernel finds room on SMs that the grid leaves free, or waits for its
+// end.  Of 190 measured splits of 16 shapes it picks ones 2.4% from the best
+// (worst 21%, 128 short sequences).  Two row tiles to a CTA pay for long
+// prefixes of many rows, where keys and values are prepared once for both:
+// 64, 8, 8192, G = 8: 265 us in 9 ranges, one row tile 285; 32, 8, 512, G = 8:
+// 34.2 and 33.1; 40, 2, 4096, G = 8: 51.2 and 47.4.
+//
+// 0 ranges: too little to share, every sequence reads the pages itself.
+// (Sequences, KV heads, pages, G = 4 unless given: read by each against once,
+// us.)  8, 8, 128: 13 and 17; 8, 8, 256: 24 and 18; 2, 8, 256: 14 and 17; 2, 8,
+// 1024: 25 and 24; 2, 8, 2048: 33 and 32; 32, 8, 32: 12 and 19; 32, 8, 64: 25
+// and 20; 64, 8, 16, G = 8: 18 and 21; 64, 8, 32, G = 8: 21 and 23; 64, 8, 64,
+// G = 8: 33 and 24; 16, 8, 64, G = 16: 17 and 24; 16, 8, 128, G = 16: 31 and 25;
+// 256, 8, 4, G = 1: 25 and 21; 256, 8, 8, G = 1: 29 and 21; 128, 1, 64, G = 8:
+// 14 and 19; 128, 1, 128, G = 8: 27 and 22; one sequence, 8, 8192: 64 and 77.
+PrefixPlan prefix_plan(int batch, int h_kv, int G, int pages) {
+  PrefixPlan plan{0, false};
+  if (batch < 2 || (long long)batch * h_kv * pages < kPfMinShared) return plan;
   const long long row_tiles =
       ((long long)batch * G + kPfRows - 1) / kPfRows;
-  const long long base = row_tiles * h_kv;
   const long long tiles = (pages + kPfPages - 1) / kPfPages;
   double best = 1e30;
-  int splits = 1;
-  for (long long s = 1; s <= tiles && s <= slots; ++s) {
-    const double waves = (double)((base * s + slots - 1) / slots);
-    const double us = waves * (2.6 * (double)((tiles + s - 1) / s) + 8.0) +
-                      1.6e-4 * (double)(s * batch * h_kv * G);
-    if (us < best * 0.999) {
-      best = us;
-      splits = (int)s;
+  for (int r = 1; r <= 2 && r <= row_tiles; ++r) {
+    const long long slots = r == 1 ? 304 : 152;  // CTAs that run at once
+    const long long base = (row_tiles + r - 1) / r * h_kv;
+    for (long long s = 1, t = tiles;;) {  // s ranges of up to t tiles
+      const long long ctas = base * s, waves = (ctas + slots - 1) / slots;
+      const double tile = r == 2 ? 2.0 : ctas > 152 ? 2.4 : 1.6;
+      const double room = (double)(waves * slots - ctas) / 88.0;
+      const double us = (double)waves * (tile * (double)t + 6.0) +
+                        1.6e-4 * (double)(s * batch * h_kv * G) +
+                        (room < 1.0 ? 2.0 * r * (1.0 - room) : 0.0);
+      if (us < best) {
+        best = us;
+        plan = {(int)s, r == 2};
+      }
+      if (t == 1) break;
+      s = (tiles + t - 2) / (t - 1);  // the fewest of fewer tiles
+      if (base * s > 2 * slots) break;
+      t = (tiles + s - 1) / s;
     }
   }
-  return splits;
+  return plan;
+}
+
+template <int R>
+static cudaError_t launch_tiles(const PfArgs &a, cudaStream_t stream) {
+  static DeviceFlags done;
+  cudaError_t e = once_per_device(done, [] {
+    return cudaFuncSetAttribute(prefix_kernel<R>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kPfSmem<R>);
+  });
+  if (e != cudaSuccess) return e;
+  const long long ctas =
+      (long long)((a.row_tiles + R - 1) / R) * a.h_kv * a.splits;
+  return launch_pdl(prefix_kernel<R>, dim3((unsigned)ctas),
+                    dim3(kPfThreads<R>), kPfSmem<R>, stream, a);
 }
 
 cudaError_t launch_prefix(const void *q, const void *records,
                           int64_t num_phys, const int32_t *table, int pages,
-                          int batch, int h_kv, int G, int splits,
+                          int batch, int h_kv, int G, PrefixPlan plan,
                           float *o_part, float2 *ml_part, int32_t *status,
                           cudaStream_t stream) {
-  static DeviceFlags done;
-  cudaError_t e = once_per_device(done, [] {
-    return cudaFuncSetAttribute(prefix_kernel,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kPfSmem);
-  });
-  if (e != cudaSuccess) return e;
   const int row_tiles = (int)(((long long)batch * G + kPfRows - 1) / kPfRows);
   const PfArgs a{static_cast<const __nv_bfloat16 *>(q),
                  static_cast<const uint8_t *>(records),
-                 num_phys, table, pages, batch, h_kv, G, row_tiles, splits,
+                 num_phys, table, pages, batch, h_kv, G, row_tiles, plan.splits,
                  o_part, ml_part, status};
-  return launch_pdl(prefix_kernel,
-                    dim3((unsigned)((long long)row_tiles * h_kv * splits)),
-                    dim3(kPfThreads), kPfSmem, stream, a);
+  return plan.wide ? launch_tiles<2>(a, stream) : launch_tiles<1>(a, stream);
 }
 
 }  // namespace locks

@@ -536,11 +536,14 @@ def test_prefix(G, np_, lens, h_kv):
 # enough pages times units that the prefix is taken once for all
 SHARED = [(256, 1, 8, 12), (240, 2, 8, 13), (31, 16, 4, 200), (6, 5, 8, 515),
           (2, 8, 8, 1543), (64, 4, 1, 400), (100, 3, 3, 83)]
+# .. and that a CTA takes two tiles of rows; an odd number of them, a last one
+# with few rows
+WIDE = [(67, 16, 2, 905), (129, 16, 4, 300)]
 
 
 @pytest.mark.parametrize("batch,G,h_kv,np_", [
     (33, 4, 2, 70), (70, 8, 1, 20), (9, 16, 3, 130), (1, 4, 8, 3100),
-    (5, 16, 1, 7001)] + SHARED)
+    (5, 16, 1, 7001)] + SHARED + WIDE)
 def test_prefix_of_many_rows(batch, G, h_kv, np_):
     # several tiles of query rows, several splits of the prefix, partial tiles
     # of both; some sequences shorter than the prefix, one empty
@@ -556,10 +559,7 @@ def test_prefix_of_many_rows(batch, G, h_kv, np_):
     check(o, lse, qn, rec, Q.decode(qn, rec, table, lens, prefix=prefix))
 
 
-@pytest.mark.parametrize("kind", ["strong", "scales", "rising", "large q",
-                                  "small q"])
-def test_shared_prefix_extremes(kind):
-    batch, G, h_kv, np_ = 31, 4, 4, 200
+def prefix_extremes(kind, batch, G, h_kv, np_):
     rng = np.random.default_rng(len(kind))
     lens = [16 * np_ + int(x) for x in rng.integers(0, 20, batch)]
     rec, prefix, table = prefix_case(rng, np_, lens, h_kv)
@@ -588,7 +588,7 @@ def test_shared_prefix_extremes(kind):
         for i, p in enumerate(prefix):
             for s in range(16):
                 rec[p, :, Q._PLACE[s]] = codes[0][:, None]
-                rec[p, :, 4096 + s] = 127 - 29 + i // 10
+                rec[p, :, 4096 + s] = 127 - 29 + 20 * i // np_
         q = torch.ones_like(q)
     o, lse, st = run_prefix(q, rec, prefix, table, lens)
     assert st == 0
@@ -598,6 +598,44 @@ def test_shared_prefix_extremes(kind):
     below = max(lens) * 2.0 ** -33 * 448 * 2.0 ** -7 if kind == "strong" else 0
     check(o, lse, qn, rec, Q.decode(qn, rec, table, lens, prefix=prefix),
           below)
+
+
+EXTREMES = ["strong", "scales", "rising", "large q", "small q"]
+
+
+@pytest.mark.parametrize("kind", EXTREMES)
+def test_shared_prefix_extremes(kind):
+    prefix_extremes(kind, 31, 4, 4, 200)
+
+
+@pytest.mark.parametrize("kind", EXTREMES)
+def test_shared_prefix_extremes_of_many_rows(kind):
+    # enough rows and pages for two row tiles to a CTA, the last one alone
+    prefix_extremes(kind, 67, 16, 2, 900)
+
+
+@pytest.mark.parametrize("batch,G,h_kv,np_", [(6, 5, 8, 515),
+                                              (67, 16, 2, 905)])
+def test_shared_prefix_repeats_itself(batch, G, h_kv, np_):
+    # buffers that are copied to while others are read: the same bits each time
+    rng = np.random.default_rng(batch)
+    lens = [16 * np_ + int(x) for x in rng.integers(0, 60, batch)]
+    rec, prefix, table = prefix_case(rng, np_, lens, h_kv)
+    q = queries(rng, batch, G * h_kv).to(DEV)
+    rec = torch.from_numpy(rec).to(DEV)
+    ws = B.new_prefix_workspace(batch, G * h_kv, h_kv, table.shape[1], np_,
+                                DEV)
+    prefix, table, lens = i32(prefix), i32(table), i32(lens)
+    differ = torch.zeros((), dtype=torch.int32, device=DEV)
+    for i in range(200):
+        o = torch.zeros_like(q)
+        lse = torch.zeros(q.shape[:2], device=DEV)
+        B.locks_prefix_decode(q, rec, prefix, table, lens, o, lse, ws)
+        if i == 0:
+            first = o.clone(), lse.clone()
+        differ += (o != first[0]).any() | (lse != first[1]).any()
+    assert int(differ) == 0
+    assert B.locks_read_status(ws) == 0
 
 
 def test_shared_prefix_reports_bad_pages():
