@@ -585,7 +585,8 @@ locks_status_t locks_prefix_decode(
     void *o_out, float *lse_out, void *workspace, size_t workspace_bytes,
     locks_stream_t stream);
 
-/* Workspace bytes of locks_prefix_decode for these sizes. */
+/* Workspace bytes of locks_prefix_decode for these sizes (a smaller batch may
+ * need more: its share of the GPU reads the prefix in more ranges). */
 locks_status_t locks_prefix_workspace_size(int batch, int h_q, int h_kv,
                                            int max_pages, int prefix_pages,
                                            size_t *bytes);
