@@ -759,13 +759,19 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
 // ---------------------------------------------------------------------------
 // launchers
 // ---------------------------------------------------------------------------
+// dynamic shared memory: what a CTA may have without its barriers, and the
+// largest batch whose positions fit beside the ring
+constexpr size_t kQdSmemMost = 227 * 1024 - 256;
+constexpr int kQdMaxBatch = 41088;
+static_assert(sizeof(uint64_t) * kQdWarps * kQdStages <= 256, "barriers");
+static_assert(kQdRing + sizeof(int) * (kQdMaxBatch + 1) <= kQdSmemMost,
+              "ring and positions");
+
 static size_t qdecode_smem(bool unit, int batch) {
   return (size_t)kQdRing + (unit ? 0 : sizeof(int) * ((size_t)batch + 1));
 }
 
-int qdecode_max_batch() {
-  return (int)((227 * 1024 - (size_t)kQdRing - 512) / sizeof(int));
-}
+int qdecode_max_batch() { return kQdMaxBatch; }
 
 template <int NT, bool UNIT>
 static cudaError_t qdecode_ready() {
@@ -773,7 +779,7 @@ static cudaError_t qdecode_ready() {
   return once_per_device(done, [] {
     return cudaFuncSetAttribute(qdecode_kernel<NT, UNIT>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                226 * 1024);
+                                (int)kQdSmemMost);
   });
 }
 
