@@ -557,7 +557,9 @@ locks_status_t locks_dequantise_kv(
  * the numbers that the records stand for.  q and o_out must be 16-byte
  * aligned.  The query takes part in fp16 after a power-of-two scale per
  * head, the weights in fp16, sums and softmax statistics in fp32.
- * LOCKS_ERR_UNSUPPORTED for a batch above 41088. */
+ * LOCKS_ERR_UNSUPPORTED for a batch above 41088, or more than 2^31 - 2^16
+ * list entries (batch * h_kv * k, or batch * h_kv * max_pages without a
+ * list). */
 locks_status_t locks_quantised_decode(
     const void *q, const void *records, int64_t num_phys_pages,
     const int32_t *page_table, const int32_t *seq_lens, const int32_t *idx,

@@ -521,8 +521,10 @@ static locks_status_t check_qdecode(const void *q, const void *records,
   if (list_len < 1) return LOCKS_ERR_INVALID_ARG;
   if (h_q / h_kv > kMaxGroup) return LOCKS_ERR_UNSUPPORTED;
   if (batch > qdecode_max_batch() || h_kv > 65535) return LOCKS_ERR_UNSUPPORTED;
+  // list entries are int32 positions, and a warp's run and window end past its
+  // last one, by up to a window and a run's rounding
   if ((long long)max_pages * kPage > 0x7fffffffLL ||
-      (long long)batch * h_kv * list_len > 0x7fffffffLL ||
+      (long long)batch * h_kv * list_len > 0x7fffffffLL - 0xffffLL ||
       (long long)batch * h_q > 0x7fffffffLL)
     return LOCKS_ERR_UNSUPPORTED;
   if (batch == 0) return LOCKS_OK;
