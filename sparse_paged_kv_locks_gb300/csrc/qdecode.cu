@@ -395,7 +395,9 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
       load_q(cur);
       q_ready = true;
     }
-    if (!q_wait(bar + st, phase)) {
+    // one verdict for the warp: its lanes' waits may end on either side of the
+    // limit, and what follows either way takes all of them
+    if (!__all_sync(0xffffffffu, q_wait(bar + st, phase))) {
       dead = true;
       break;
     }
