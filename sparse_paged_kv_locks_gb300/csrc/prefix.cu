@@ -657,12 +657,6 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
             scores(t, j + 1);
           }
         }
-      if (*(volatile int *)&sh.dead && elect_one()) {
-        // give what is in flight a last, bounded chance to finish
-        set_status(a.status, LOCKS_DEV_TIMEOUT);
-        mma_commit(&sh.drain);
-        q_wait(&sh.drain, 0);
-      }
     } else if (wid == kKeys) {
       // ------------------------------------------------------------ keys
       int copied = 0;  // tiles
@@ -840,11 +834,20 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
   __syncwarp();
   tm_fence_before();
   __syncthreads();
-  if (wid == kProducts)
+  if (wid == kProducts) {
+    // some role's wait gave up, the last of them that for the last products:
+    // say so, and give what is in flight a last, bounded chance to finish
+    if (*(volatile int *)&sh.dead && elect_one()) {
+      set_status(a.status, LOCKS_DEV_TIMEOUT);
+      mma_commit(&sh.drain);
+      q_wait(&sh.drain, 0);
+    }
+    __syncwarp();
     asm volatile(
         "tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tm),
         "r"(R * kPfColumns)
         : "memory");
+  }
 }
 
 // ---------------------------------------------------------------------------
