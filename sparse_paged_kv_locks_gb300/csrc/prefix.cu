@@ -353,38 +353,41 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
   const int nt = min(R, a.row_tiles - rt);
   const int rows = a.batch * a.G;
 
-  if (wid == kProducts) {
+  if (wid == kProducts && lane == 0) {
+    for (int i = 0; i < R; ++i) {
+      mbar_init(sh.q_full + i, 4);
+      mbar_init(sh.qk_done + i, 1);
+      mbar_init(sh.p_full + i, 4);
+      mbar_init(sh.o_done + i, 1);
+      mbar_init(sh.k_raw + i, 1);
+      mbar_init(sh.k_full + i, 1);
+      mbar_init(sh.k_free + i, 1);
+      for (int w = 0; w < kPfWiden; ++w) mbar_init(sh.v_raw[w] + i, 1);
+      mbar_init(sh.v_full + i, kPfWiden);
+      mbar_init(sh.v_free + i, 1);
+    }
+    mbar_init(sh.info, kPfWiden);
+    mbar_init(sh.info + 1, kPfWiden);
+    mbar_init(&sh.drain, 1);
+    sh.dead = 0;
+    fence_mbar_init();
+  }
+  __syncwarp();
+  // Tensor memory is taken after the kernels before this one have ended: a
+  // kernel that let this one start early and then takes its own, on an SM that
+  // both fit, would wait for columns that are held here until it has ended.
+  pdl_wait();
+  if (wid == kProducts)
     asm volatile(
         "tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n"
         " tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::"r"(
             smem_u32(&sh.tmem)),
         "r"(R * kPfColumns)
         : "memory");
-    if (lane == 0) {
-      for (int i = 0; i < R; ++i) {
-        mbar_init(sh.q_full + i, 4);
-        mbar_init(sh.qk_done + i, 1);
-        mbar_init(sh.p_full + i, 4);
-        mbar_init(sh.o_done + i, 1);
-        mbar_init(sh.k_raw + i, 1);
-        mbar_init(sh.k_full + i, 1);
-        mbar_init(sh.k_free + i, 1);
-        for (int w = 0; w < kPfWiden; ++w) mbar_init(sh.v_raw[w] + i, 1);
-        mbar_init(sh.v_full + i, kPfWiden);
-        mbar_init(sh.v_free + i, 1);
-      }
-      mbar_init(sh.info, kPfWiden);
-      mbar_init(sh.info + 1, kPfWiden);
-      mbar_init(&sh.drain, 1);
-      sh.dead = 0;
-      fence_mbar_init();
-    }
-  }
   tm_fence_before();
   __syncthreads();
   tm_fence_after();
   const uint32_t tm = sh.tmem;
-  pdl_wait();
   pdl_trigger();
 
   const int tile = wid >> 2;  // row tile of a softmax warp
