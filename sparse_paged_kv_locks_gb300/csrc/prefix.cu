@@ -388,6 +388,8 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
   __syncthreads();
   tm_fence_after();
   const uint32_t tm = sh.tmem;
+  // after the wait, never before: the kernel of the sequences' own pages starts
+  // here and does not wait for the kernels before this one by itself
   pdl_trigger();
 
   const int tile = wid >> 2;  // row tile of a softmax warp

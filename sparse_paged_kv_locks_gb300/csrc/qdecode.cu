@@ -73,9 +73,13 @@ struct QdArgs {
   float2 *ml_part;   // [slot][G] (m, sum of weights)
   int *meta;         // run length, then the sequences' first positions
   int32_t *status;
-  // launched beside the kernel that takes those pages, which waited for
-  // everything before it: sequences at least as long as they are leave them
-  // out of their lists, and this kernel waits for that one only at its end
+  // launched beside the kernel that takes those pages: sequences at least as
+  // long as they are leave them out of their lists, and this kernel waits for
+  // that one only at its end.  What it reads until then was written by kernels
+  // before both.  Every CTA of that kernel waits for those, which makes their
+  // writes visible in L2, before it lets this one start, and none of the reads
+  // goes through an L1 that could hold older values: queries, lengths and
+  // tables by loads that bypass it, records by bulk copies.
   bool beside;
 };
 
@@ -101,9 +105,9 @@ __device__ __forceinline__ QEntry q_resolve(const QdArgs &a,
   if (a.idx) {
     // the table entry is read beside the length it is checked against, where
     // the table has one
-    pg = __ldg(a.idx + (size_t)e.u * a.k + pg);
+    pg = __ldcg(a.idx + (size_t)e.u * a.k + pg);
     if (pg < 0) return e;
-    ph = pg < a.max_pages ? __ldg(table + pg) : -1;
+    ph = pg < a.max_pages ? __ldcg(table + pg) : -1;
   }
   const int L = checked_len(a.seq_lens, b, a.max_pages, a.status);
   const int n = (L + kPage - 1) / kPage;
@@ -117,7 +121,7 @@ __device__ __forceinline__ QEntry q_resolve(const QdArgs &a,
     if (pg >= n) return e;  // (unit form: lists as long as the table)
     if (pg < a.prefix_pages) table = a.prefix;
   }
-  if (!a.idx) ph = __ldg(table + pg);
+  if (!a.idx) ph = __ldcg(table + pg);
   if (ph < 0 || ph >= a.num_phys) {
     set_status(a.status, LOCKS_DEV_BAD_PAGE_ID);
     return e;
@@ -270,7 +274,7 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {  // 16-byte loads: group t + 4 (i / 2)
         const uint4 v =
-            in ? __ldg(reinterpret_cast<const uint4 *>(
+            in ? __ldcg(reinterpret_cast<const uint4 *>(
                      qu + (8 * nt + g) * kDim + 16 * (t + 4 * (i >> 1)) +
                      8 * (i & 1)))
                : make_uint4(0u, 0u, 0u, 0u);

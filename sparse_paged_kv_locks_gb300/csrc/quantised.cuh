@@ -135,7 +135,7 @@ __device__ __forceinline__ void fence_to_async() {
 
 __device__ __forceinline__ int checked_len(const int32_t *seq_lens, int b,
                                            int max_pages, int32_t *status) {
-  const int L = __ldg(seq_lens + b);
+  const int L = __ldcg(seq_lens + b);  // not by L1: see QdArgs::beside
   const int top = max_pages * kPage;
   if (L < 0 || L > top) {
     set_status(status, LOCKS_DEV_BAD_SEQ_LEN);

@@ -74,3 +74,57 @@ def test_largest_batches(batch, np_):
             assert np.isneginf(got).all()
         else:
             assert (np.abs(got - wlse[k]) <= 1e-4).all()
+
+
+# ---------------------------------------------------------------------------
+# order
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("batch,np_", [(62, 200), (3, 9)])
+def test_steps_back_to_back_see_the_latest_inputs(batch, np_):
+    # queries, lengths, tables and rows change right before every call, with
+    # nothing between the kernels; the kernel of the sequences' own pages
+    # starts before the prefix's has ended and reads them
+    rng = np.random.default_rng(batch)
+    h_kv, G, steps, max_pages = 2, 4, 24, np_ + 5
+    P = np_ + batch * 5
+    rec = torch.from_numpy(records(rng, P, h_kv)).to(DEV)
+    prefix = i32(rng.permutation(np_))
+    tables = i32(np.stack([np.concatenate(
+        [np.full((batch, np_), -7),
+         np_ + rng.permutation(batch * 5).reshape(batch, 5)], 1)
+        for _ in range(steps)]))
+    lens = i32(16 * np_ + rng.integers(0, 70, (steps, batch)))
+    q = torch.from_numpy(rng.standard_normal((steps, batch, h_kv * G, 128))) \
+        .to(DEV, torch.bfloat16)
+    kv = torch.from_numpy(rng.standard_normal((steps, batch, h_kv, 128))) \
+        .to(DEV, torch.bfloat16)
+    seq = torch.arange(batch, dtype=torch.int32, device=DEV)
+
+    def run(wait):
+        cache, table, L = rec.clone(), tables[0].clone(), lens[0].clone()
+        row, qi = kv[0].clone(), q[0].clone()
+        ws = B.new_prefix_workspace(batch, h_kv * G, h_kv, max_pages, np_, DEV)
+        outs = [(torch.empty_like(qi), torch.empty(batch, h_kv * G,
+                                                   device=DEV))
+                for _ in range(steps)]
+        torch.cuda.synchronize()
+        for i, (o, lse) in enumerate(outs):
+            for to, new in ((table, tables[i]), (row, kv[i]), (qi, q[i]),
+                            (L, lens[i])):
+                to.copy_(new)
+            B.locks_quantise_kv(row, row, seq, L, table, cache)
+            if wait:
+                torch.cuda.synchronize()
+            L.add_(1)
+            if wait:
+                torch.cuda.synchronize()
+            B.locks_prefix_decode(qi, cache, prefix, table, L, o, lse, ws)
+            if wait:
+                torch.cuda.synchronize()
+        assert B.locks_read_status(ws) == 0
+        return outs
+
+    want = run(True)
+    for _ in range(5):
+        for (o, lse), (wo, wl) in zip(run(False), want):
+            assert torch.equal(o, wo) and torch.equal(lse, wl)
