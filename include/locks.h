@@ -587,8 +587,9 @@ locks_status_t locks_prefix_decode(
     void *o_out, float *lse_out, void *workspace, size_t workspace_bytes,
     locks_stream_t stream);
 
-/* Workspace bytes of locks_prefix_decode for these sizes (a smaller batch may
- * need more: its share of the GPU reads the prefix in more ranges). */
+/* Workspace bytes of locks_prefix_decode for these sizes.  Never less for a
+ * larger batch, prefix or table: the size for the largest of each serves all
+ * smaller ones with the same heads. */
 locks_status_t locks_prefix_workspace_size(int batch, int h_q, int h_kv,
                                            int max_pages, int prefix_pages,
                                            size_t *bytes);

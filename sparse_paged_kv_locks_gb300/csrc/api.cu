@@ -573,7 +573,7 @@ static PrefixRegion prefix_region(uint8_t *at, int batch, int h_q, int h_kv,
   if (pages == 0 || batch == 0) return {{0, false}, nullptr, nullptr, 0};
   const PrefixPlan plan = prefix_plan(batch, h_kv, h_q / h_kv, pages);
   if (plan.splits == 0) return {plan, nullptr, nullptr, 0};
-  const size_t rows = (size_t)plan.splits * batch * h_q;
+  const size_t rows = prefix_rows(batch, h_kv, h_q / h_kv, pages);
   const size_t sums = round_up(rows * kDim * 4, 256);
   return {plan, reinterpret_cast<float *>(at),
           reinterpret_cast<float2 *>(at + sums),

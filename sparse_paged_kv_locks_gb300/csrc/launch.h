@@ -201,6 +201,8 @@ struct PrefixPlan {
   bool wide;
 };
 PrefixPlan prefix_plan(int batch, int h_kv, int G, int pages);
+// rows of partials that any plan up to these sizes stays within
+size_t prefix_rows(int batch, int h_kv, int G, int pages);
 cudaError_t launch_prefix(const void *q, const void *records,
                           int64_t num_phys, const int32_t *table, int pages,
                           int batch, int h_kv, int G, PrefixPlan plan,

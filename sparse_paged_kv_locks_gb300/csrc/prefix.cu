@@ -910,6 +910,19 @@ PrefixPlan prefix_plan(int batch, int h_kv, int G, int pages) {
   return plan;
 }
 
+// Rows of partials that the workspace has room for: no plan up to these sizes
+// has more, whatever its number of ranges, so that a workspace of one batch and
+// prefix serves all smaller ones.  A plan of more than one range has at most
+// 2 * 304 (or 152) CTAs of 128 (256) rows each, and never more ranges than
+// tiles.
+size_t prefix_rows(int batch, int h_kv, int G, int pages) {
+  if (batch < 2 || (long long)batch * h_kv * pages < kPfMinShared) return 0;
+  const size_t rows = (size_t)batch * h_kv * G;
+  const size_t tiles = ((size_t)pages + kPfPages - 1) / kPfPages;
+  const size_t most = 2 * 304 * kPfRows;
+  return tiles * rows < most ? tiles * rows : rows > most ? rows : most;
+}
+
 template <int R>
 static cudaError_t launch_tiles(const PfArgs &a, cudaStream_t stream) {
   static DeviceFlags done;
