@@ -556,7 +556,10 @@ locks_status_t locks_dequantise_kv(
  * (idx NULL: every page), outputs, workspace and status bits, with K and V
  * the numbers that the records stand for.  q and o_out must be 16-byte
  * aligned.  The query takes part in fp16 after a power-of-two scale per
- * head, the weights in fp16, sums and softmax statistics in fp32.
+ * head, sums and softmax statistics in fp32.  Weights have 11 bits, whatever
+ * the value rows' scales: of rows within 2^8 of the largest scale, weights
+ * below 2^-22 of the largest lose bits, which moves an output by at most 2^-25
+ * of the largest weight times the sum of |v| in its dim.
  * LOCKS_ERR_UNSUPPORTED for a batch above 41088, or more than 2^31 - 2^16
  * list entries (batch * h_kv * k, or batch * h_kv * max_pages without a
  * list). */

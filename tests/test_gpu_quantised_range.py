@@ -128,3 +128,204 @@ def test_steps_back_to_back_see_the_latest_inputs(batch, np_):
     for _ in range(5):
         for (o, lse), (wo, wl) in zip(run(False), want):
             assert torch.equal(o, wo) and torch.equal(lse, wl)
+
+
+# ---------------------------------------------------------------------------
+# values of very different scales
+# ---------------------------------------------------------------------------
+# Tolerances, per output element, from the formats:
+#   * o rounded to bf16 once: half a step, 2^-8 of it
+#   * every weight rounded to 11 bits or more, whatever its size, exponentials
+#     and fp32 sums: 2^-11 + 2^-13 of each term p |v|
+#   * rows whose scale is within 2^8 of the largest keep fp16 weights, off by
+#     2^-25 at most where the largest term's is 2^8 or more: 2^-33 of the
+#     largest weight times the largest scale, 2^-25 of it times the row's own
+#   * scores off by dx each: a weight by expm1(2 max dx) of it, the largest
+#     weight by as much of all the others'
+#   * dx: 128 products and sums, 2^-24 each; fp32 exponents of numbers up to
+#     |x| + 64, twice; the query as the call takes it (`query`: its step, as a
+#     share of the row's largest element)
+#   * lse: max dx, fp32 rounding
+# Outputs in dims where the far larger rows hold zeros are sums of the others
+# alone, so these hold element by element, not against the row's largest.
+def bounds(q, K, V, query):
+    G = q.shape[0]
+    if K.shape[0] == 0:
+        return (np.zeros((G, 128)), np.full(G, -np.inf), np.zeros((G, 128)),
+                np.zeros(G))
+    x = q @ K.T / math.sqrt(128)
+    dx = (2.0 ** -17 * np.abs(q) @ np.abs(K).T + query *
+          np.abs(q).max(1, keepdims=True) * np.abs(K).sum(1)) / math.sqrt(128)
+    dx = (dx + 2.0 ** -22 * (np.abs(x) + 64)).max(1)
+    top = x.max(1, keepdims=True)
+    w = np.exp(x - top)
+    total = w.sum(1, keepdims=True)
+    p = w / total
+    o, lse = p @ V, (top + np.log(total))[:, 0]
+    absv = np.abs(V)
+    best = p.argmax(1)
+    rest = p.copy()
+    rest[np.arange(G), best] = 0.0
+    move = np.expm1(np.minimum(2 * dx, 50.0))[:, None]
+    tol = 2.0 ** -8 * np.abs(o) + (2.0 ** -11 + 2.0 ** -13) * (p @ absv) + \
+        2.0 ** -25 * p.max(1)[:, None] * absv.sum(0) + \
+        move * (rest @ absv + rest.sum(1)[:, None] * absv[best]) + 1e-36
+    return o, lse, tol, dx + 2.0 ** -20 * np.abs(lse) + 2.0 ** -20
+
+
+def expect(got, q, rec, tables, lens, idx=None, prefix=None, query=2.0 ** -32):
+    """Every output of a decode against the definition in 64 bits."""
+    got_o, got_lse = (t.double().cpu().numpy() for t in got)
+    h_kv = rec.shape[1]
+    G = q.shape[1] // h_kv
+    np_ = 0 if prefix is None else len(prefix)
+    for h in range(h_kv):
+        if np_:
+            K0, V0 = Q.read(rec[prefix, h])
+            K0, V0 = K0.reshape(-1, 128), V0.reshape(-1, 128)
+        for b, n in enumerate(lens):
+            n = int(n)
+            pages = range(np_, -(-n // 16)) if idx is None else idx[b, h]
+            K, V = Q.tokens(rec, tables[b], h, pages, n)
+            if np_:
+                K = np.concatenate([K0[:n], K])
+                V = np.concatenate([V0[:n], V])
+            sl = slice(h * G, (h + 1) * G)
+            o, lse, tol, ltol = bounds(q[b, sl], K, V, query)
+            off = np.abs(got_o[b, sl] - o)
+            assert (off <= tol).all(), (b, h, (off / tol).max(),
+                                        np.argwhere(~(off <= tol))[:4])
+            if K.shape[0] == 0:
+                assert np.isneginf(got_lse[b, sl]).all()
+            else:
+                assert (np.abs(got_lse[b, sl] - lse) <= ltol).all(), (b, h)
+
+
+def layout(rng, lens, h_kv, centre, room=2, np_=0):
+    """Records with value scales around 2^centre, tables; NaN and absurd
+    scales past each sequence's end."""
+    batch = len(lens)
+    max_pages = max(1, -(-max(lens) // 16)) + room
+    P = batch * (max_pages - np_) + np_ + 3
+    perm = rng.permutation(P).astype(np.int32)
+    prefix = perm[:np_]
+    tables = np.full((batch, max_pages), -77, np.int32)
+    tables[:, np_:] = perm[np_:np_ + batch * (max_pages - np_)].reshape(
+        batch, -1)
+    rec = records(rng, P, h_kv)
+    rec[..., 4112:] = 127 + centre + rng.integers(-2, 3, rec[..., 4112:].shape)
+    for b, n in enumerate(lens):
+        if n % 16 and n // 16 >= np_:
+            r = rec[tables[b, n // 16]]
+            for s in range(n % 16, 16):
+                r[:, Q._PLACE[s]] = r[:, 2048 + Q._PLACE[s]] = 0x7F
+                r[:, [4096 + s, 4112 + s]] = 255
+    return rec, tables, prefix
+
+
+def plant(rec, page, slot, exponent, dims=(17,), q=None):
+    """Gives a row the value 448 * 2^exponent in `dims` and zero elsewhere,
+    and with `q` [h_kv][128] a key that scores high with these."""
+    for h in range(rec.shape[1]):
+        r = rec[page, h]
+        r[2048 + Q._PLACE[slot]] = 0
+        r[2048 + Q._PLACE[slot, list(dims)]] = 0x7E
+        r[4112 + slot] = 127 + exponent
+        if q is not None:
+            codes, e = Q.quantise_rows(q[h][None])
+            r[Q._PLACE[slot]] = codes[0]
+            r[4096 + slot] = e[0] + 127
+
+
+def normal(rng, *shape):
+    return torch.from_numpy(rng.standard_normal(shape)).to(torch.bfloat16)
+
+
+def run_lists(q, rec, tables, lens, idx=None):
+    batch, h_q, _ = q.shape
+    max_pages = tables.shape[1]
+    k = max_pages if idx is None else idx.shape[2]
+    o = torch.full((batch, h_q, 128), 7.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((batch, h_q), 7.0, device=DEV)
+    ws = B.new_workspace(batch, h_q, rec.shape[1], max_pages, k, DEV)
+    B.locks_quantised_decode(q.to(DEV), torch.from_numpy(rec).to(DEV),
+                             i32(tables), i32(lens),
+                             None if idx is None else i32(idx), k, o, lse, ws)
+    assert B.locks_read_status(ws) == 0
+    return o, lse
+
+
+def lists(rng, lens, h_kv, k):
+    idx = np.full((len(lens), h_kv, k), -1, np.int32)
+    for b, n in enumerate(lens):
+        n = -(-n // 16)
+        for h in range(h_kv):
+            some = rng.permutation(n)[:k]
+            some[:2] = [0, n - 1]
+            some = np.unique(some)
+            idx[b, h, :len(some)] = some
+    return idx
+
+
+FORMS = [([640, 500, 17], 2, 0, 0), ([900, 33], 2, 600, 0),
+         ([2000, 1500], 2, 2, 40)]   # lens, h_kv, room, k
+
+
+@pytest.mark.parametrize("G", [4, 16])
+@pytest.mark.parametrize("lens,h_kv,room,k", FORMS)
+@pytest.mark.parametrize("centre,high", [(-9, 15), (-9, 31), (-30, 31)])
+@pytest.mark.parametrize("strong", [False, True])
+def test_one_value_far_above_the_rest(G, lens, h_kv, room, k, centre, high,
+                                      strong):
+    # scales 24, 40 and 61 apart (a CTA to a unit, runs over all lists,
+    # clusters): the high row first, in the middle and last, among ordinary
+    # weights or with most of the weight of one query head
+    rng = np.random.default_rng(G + high)
+    rec, tables, _ = layout(rng, lens, h_kv, centre, room)
+    q = normal(rng, len(lens), G * h_kv, 128)
+    qn = q.double().numpy()
+    for b, n in enumerate(lens):
+        t = (0, n // 2, n - 1)[b]
+        plant(rec, tables[b, t // 16], t % 16, high, q=0.7 * qn[b, ::G]
+              if strong else None)
+    idx = lists(rng, lens, h_kv, k) if k else None
+    expect(run_lists(q, rec, tables, lens, idx), qn, rec, tables, lens, idx)
+
+
+@pytest.mark.parametrize("G", [1, 8, 12])
+@pytest.mark.parametrize("room", [0, 700])
+def test_values_of_the_whole_scale_range(G, room):
+    # every row its own scale in -32 .. 31
+    rng = np.random.default_rng(G)
+    lens = [500, 31, 700]
+    rec, tables, _ = layout(rng, lens, 2, 0, room)
+    live = rec[..., 4112:] < 255
+    rec[..., 4112:] = np.where(
+        live, 127 + rng.integers(-32, 32, live.shape), 255)
+    # few codes that are not zero, so that every dim has rows of its own
+    codes = rec[..., 2048:4096]
+    codes[rng.random(codes.shape) < 0.99] = 0
+    q = normal(rng, 3, G * 2, 128)
+    qn = q.double().numpy()
+    # rubbish past the ends again
+    for b, n in enumerate(lens):
+        for s in range(n % 16, 16):
+            rec[tables[b, n // 16], :, 2048 + Q._PLACE[s]] = 0x7F
+    expect(run_lists(q, rec, tables, lens), qn, rec, tables, lens)
+
+
+@pytest.mark.parametrize("value", [math.inf, -math.inf, 1e9, 1e8, 1e6])
+def test_attention_over_rows_with_one_huge_number(value):
+    # written by the framework itself: infinities are kept as +-448 * 2^31
+    rng = np.random.default_rng(5)
+    n, h_kv, G = 512, 2, 4
+    k, v = normal(rng, n, h_kv, 128), normal(rng, n, h_kv, 128)
+    v[100, :, 5] = value
+    table = i32(np.arange(32)[None])
+    cache = B.new_quantised_cache(32, h_kv, DEV)
+    B.locks_quantise_kv(k.to(DEV), v.to(DEV), i32([0] * n), i32(range(n)),
+                        table, cache)
+    rec, tables = cache.cpu().numpy(), table.cpu().numpy()
+    q = normal(rng, 1, G * h_kv, 128)
+    expect(run_lists(q, rec, tables, [n]), q.double().numpy(), rec, tables,
+           [n])
