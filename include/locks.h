@@ -582,7 +582,10 @@ locks_status_t locks_quantised_decode(
  *   prefix_pages  0 .. max_pages (0: locks_quantised_decode without a list)
  *   workspace     >= locks_prefix_workspace_size bytes, its first int32 the
  *                 device status word, as for the other calls
- * Other arguments, numerics and errors as locks_quantised_decode. */
+ * Other arguments and errors as locks_quantised_decode, and so the weights; the
+ * query of the shared pages takes part as the sum of two e4m3 numbers, off by
+ * at most 2^-18 of its head's largest element where it is 2^-11 of that or
+ * less. */
 locks_status_t locks_prefix_decode(
     const void *q, const void *records, int64_t num_phys_pages,
     const int32_t *prefix_table, int prefix_pages, const int32_t *page_table,

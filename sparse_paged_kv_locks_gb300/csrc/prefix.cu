@@ -15,8 +15,9 @@
 // of the row's largest element and off by at most 2^-10, 2^-18 of it, below.
 // A key's scale multiplies its column of scores.  Value codes are widened to
 // fp16, a page's rows scaled by 2^(e - E), E the largest exponent of the
-// page: exact for rows within 2^15 of the page's largest (and below that off
-// by 2^-25 of the page's largest code).  E joins the weights' exponent.
+// page, which joins the weights' exponent: exact, since a tile with rows more
+// than 2^8 below the largest scale so far takes another form (far_tile: codes
+// and weights in bf16, the weights as hi + lo).
 //
 // Rows of a record are swizzled by f(s) = (s & 6) ^ 5 (s & 1), rows of the
 // tensor core's operand by s & 7.  The two agree on even rows; an odd row's
@@ -82,6 +83,12 @@ constexpr float kPfScale = 0.12751743074602467f;  // log2(e) / sqrt(128)
 constexpr long long kPfMinShared = 12288;
 constexpr float kPfLift = 8.f;   // as in the single-token kernel
 constexpr float kPfSlack = 7.f;
+// A tile with value rows more than 2^8 below the largest scale so far takes its
+// weights and values in bf16 (far_tile).  Twice the time, for tiles after an
+// outlier's alone: with an infinity in its first page a 128K prefix for 64
+// sequences takes 620 us instead of 276 (the range that holds it is the last to
+// end), one of 32K for 32 49 us instead of 47.
+constexpr uint32_t kPfSpread = 8;
 
 // ---------------------------------------------------------------------------
 // tcgen05
@@ -100,6 +107,8 @@ constexpr uint32_t kPfDescS =
     1u << 4 | ((uint32_t)kPfTile >> 3) << 17 | (128u >> 4) << 24;
 constexpr uint32_t kPfDescO =
     1u << 4 | 1u << 16 | ((uint32_t)kDim >> 3) << 17 | (128u >> 4) << 24;
+// .. both operands bf16
+constexpr uint32_t kPfDescFar = kPfDescO | 1u << 7 | 1u << 10;
 
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b,
                                        uint32_t desc, bool add) {
@@ -284,12 +293,17 @@ struct PfShared {
   float k_scale[2][kPfTile];
   float v_exp[2][kPfPages], v_inv[2][kPfPages];
   uint32_t there[2][kPfWiden];
+  // whether the tile is a far one, then the scales of its values by token; the
+  // widening warps' largest and least of them
+  alignas(16) uint8_t v_token[2][kPfTile];
+  int far[2];
+  uint2 range[2][kPfWiden];
   uint32_t tmem;
   int dead;
   uint64_t q_full[R], qk_done[R], p_full[R], o_done[R];      // of a row tile
   uint64_t k_raw[R], k_full[R], k_free[R];                   // of a buffer
   uint64_t v_raw[kPfWiden][R], v_full[R], v_free[R];
-  uint64_t info[2], drain;
+  uint64_t info[2], ranges[2], drain;
 };
 
 // one lane of the warp, for what a warp does once
@@ -368,6 +382,8 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
     }
     mbar_init(sh.info, kPfWiden);
     mbar_init(sh.info + 1, kPfWiden);
+    mbar_init(sh.ranges, kPfWiden);
+    mbar_init(sh.ranges + 1, kPfWiden);
     mbar_init(&sh.drain, 1);
     sh.dead = 0;
     fence_mbar_init();
@@ -455,6 +471,82 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
         tm + tile * kPfColumns + ((uint32_t)((wid & 3) * 32) << 16);
     float m = -INFINITY, l = 0.f;
     bool ok = true;
+    // rescales the sums in tensor memory
+    auto rescale = [&](float fall) {
+      for (int k = 0; k < 8; ++k) {
+        uint32_t o[16];
+        tm_ld16(o, mine + kPfColO + 16 * k);
+        tm_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          o[i] = __float_as_uint(__uint_as_float(o[i]) * fall);
+        tm_st16(mine + kPfColO + 16 * k, o);
+      }
+    };
+    // A far tile: every token's own value scale in its weight (so that the
+    // reference is the largest term's, and no page's rows are rounded beside a
+    // larger one), the weights as hi + lo in bf16, whose range is fp32's: 16
+    // bits at any size.  Hi and lo of a page lie over the 16 columns of its
+    // scores, 8 columns each.
+    auto far_tile = [&](int par, uint32_t there, bool sums) {
+      auto score = [&](uint32_t s, int t, uint32_t e) -> float {
+        return fmaf(__uint_as_float(s) * sh.k_scale[par][t], f,
+                    (float)((int)e - 127));
+      };
+      auto scale = [&](const uint4 &e, int i) -> uint32_t {
+        const uint32_t w = i < 4 ? e.x : i < 8 ? e.y : i < 12 ? e.z : e.w;
+        return w >> 8 * (i & 3) & 255u;
+      };
+      const uint4 *scales = reinterpret_cast<const uint4 *>(sh.v_token[par]);
+      float top = -INFINITY;
+#pragma unroll 1
+      for (int pg = 0; pg < kPfPages; ++pg) {
+        uint32_t s[16];
+        tm_ld16(s, mine + 16 * pg);
+        tm_wait_ld();
+        const uint4 e = scales[pg];
+        if (there >> pg & 1) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            top = fmaxf(top, score(s[i], kPage * pg + i, scale(e, i)));
+        }
+      }
+      const bool raise = top > m + kPfSlack;
+      if (__any_sync(0xffffffffu, raise)) {
+        const float to = raise ? top : m;
+        const float fall = to == m ? 1.f : ex2_fast(m - to);
+        m = to;
+        l *= fall;
+        if (sums) rescale(fall);
+      }
+#pragma unroll 1
+      for (int pg = 0; pg < kPfPages; ++pg) {
+        uint32_t s[16], w[16];
+        tm_ld16(s, mine + 16 * pg);
+        tm_wait_ld();
+        const uint4 e = scales[pg];
+        const bool here = there >> pg & 1;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float u[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int t = 2 * i + k;
+            const uint32_t ev = scale(e, t);
+            u[k] = here ? ex2_fast(score(s[t], kPage * pg + t, ev) -
+                                   (m - kPfLift))
+                        : 0.f;
+            if (here) l = fmaf(u[k], __uint_as_float((254u - ev) << 23), l);
+          }
+          const __nv_bfloat162 hi = __floats2bfloat162_rn(u[0], u[1]);
+          const __nv_bfloat162 lo = __floats2bfloat162_rn(
+              u[0] - __low2float(hi), u[1] - __high2float(hi));
+          w[i] = *reinterpret_cast<const uint32_t *>(&hi);
+          w[8 + i] = *reinterpret_cast<const uint32_t *>(&lo);
+        }
+        tm_st16(mine + 16 * pg, w);
+      }
+    };
     for (int j = 0; j < n; ++j) {
       const int par = j & 1;
       // with S(j) all products before it, among them O(j - 1), are done
@@ -464,6 +556,10 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
       if (!ok) break;
       tm_fence_after();
       const uint32_t there = sh.there[par][0] | sh.there[par][1];
+      const bool far = sh.far[par];
+      if (far)
+        far_tile(par, there, j > 0);
+      else
       // 64 columns at a time: their weights go over the scores they come
       // from, in columns that have been read
       for (int c = 0; c < 2; ++c) {
@@ -516,15 +612,7 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
             }
             tm_st16(mine + 16 * k, w);
           }
-          for (int k = 0; k < 8 && j > 0; ++k) {
-            uint32_t o[16];
-            tm_ld16(o, mine + kPfColO + 16 * k);
-            tm_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              o[i] = __float_as_uint(__uint_as_float(o[i]) * fall);
-            tm_st16(mine + kPfColO + 16 * k, o);
-          }
+          if (j > 0) rescale(fall);
         }
         uint32_t w[32];
         const uint64_t ff = pack2(f, f);
@@ -630,14 +718,22 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
         }
         __syncwarp();
       };
-      auto weighted = [&](int t, int j) {
+      auto weighted = [&](int t, int j, int far) {
         if (elect_one()) {
           const uint64_t v = dv + j % R * (2 * kPfBlock >> 4);
           const uint32_t at = tm + t * kPfColumns;
+          if (far) {  // hi and lo of each page
+#pragma unroll 1
+            for (int kk = 0; kk < 2 * kPfTile / 16; ++kk)
+              mma_ts(at + kPfColO, at + 8 * kk,
+                     v + (kk >> 1) * (kPage * 128 >> 4), kPfDescFar,
+                     j > 0 || kk > 0);
+          } else {
 #pragma unroll
-          for (int kk = 0; kk < kPfTile / 16; ++kk)
-            mma_ts(at + kPfColO, at + 8 * kk, v + kk * (kPage * 128 >> 4),
-                   kPfDescO, j > 0 || kk > 0);
+            for (int kk = 0; kk < kPfTile / 16; ++kk)
+              mma_ts(at + kPfColO, at + 8 * kk, v + kk * (kPage * 128 >> 4),
+                     kPfDescO, j > 0 || kk > 0);
+          }
           if (t == nt - 1) mma_commit(sh.v_free + j % R);
           if (j == n - 1) mma_commit(sh.o_done + t);
         }
@@ -646,12 +742,14 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
       for (int j = -1; j < n && ok; ++j)
         for (int t = 0; t < nt; ++t) {
           if (j >= 0) {
-            ok = (t > 0 || pf_wait_ring(sh, sh.v_full, j)) &&
-                 pf_wait(sh, sh.p_full + t, j & 1);
+            ok = t > 0 || pf_wait_ring(sh, sh.v_full, j);
+            // (under the wait for the weights: 2 us of 276)
+            const int far = sh.far[j & 1];
+            ok = ok && pf_wait(sh, sh.p_full + t, j & 1);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tm_fence_after();
-            weighted(t, j);
+            weighted(t, j, far);
           }
           if (j + 1 < n) {
             ok = (t > 0 || pf_wait_ring(sh, sh.k_full, j + 1)) &&
@@ -742,17 +840,11 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
       for (int j = 0; j < R; ++j)
         there[j] = j < n ? copy_values(page(j, first + lane)) : 0u;
       int ph = page(R, first + lane);
+      uint32_t top_e = 0;  // largest scale so far
       for (int j = 0; j < n; ++j) {
         ok = pf_wait_ring(sh, sh.v_raw[own], j);
         if (!__all_sync(0xffffffffu, ok)) break;
         const uint32_t from = mine + j % R * kPfRaw;
-        uint4 raw[4 * kPfOwn];
-#pragma unroll
-        for (int u = 0; u < 4 * kPfOwn; ++u) {
-          const int sl = 4 * (u & 3) + s4;
-          raw[u] = lds128(from + (u >> 2) * kPfRest + sl * kDim +
-                          16 * q_group(c, sl));
-        }
         // lane 16 i + slot: exponents of rows of pages i and 2 + i
         uint32_t ke[kPfOwn / 2], ve[kPfOwn / 2];
 #pragma unroll
@@ -765,10 +857,33 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
                        : "=r"(ve[i])
                        : "r"(at + (kQOffVE - kQOffV)));
         }
+        // The largest and the least scale of these pages, for both warps.  (The
+        // place of j - 2: the other warp has read it, or it had not come to the
+        // range of j - 1.)
+        const uint32_t now = there[0];
+        uint32_t most = 0, least = 255;
+#pragma unroll
+        for (int i = 0; i < kPfOwn / 2; ++i)
+          if (now >> (2 * i + (lane >> 4)) & 1) {
+            most = max(most, ve[i]);
+            least = min(least, ve[i]);
+          }
+        most = __reduce_max_sync(0xffffffffu, most);
+        least = __reduce_min_sync(0xffffffffu, least);
+        if (lane == 0) {
+          sh.range[j & 1][own] = make_uint2(most, least);
+          mbar_arrive(sh.ranges + (j & 1));
+        }
+        uint4 raw[4 * kPfOwn];
+#pragma unroll
+        for (int u = 0; u < 4 * kPfOwn; ++u) {
+          const int sl = 4 * (u & 3) + s4;
+          raw[u] = lds128(from + (u >> 2) * kPfRest + sl * kDim +
+                          16 * q_group(c, sl));
+        }
         // all has been read before the next copy is written there
         fence_to_async();
         __syncwarp();
-        const uint32_t now = there[0];
         if (copied < n) {
           if (R > 1) there[0] = there[R - 1];
           there[R - 1] = copy_values(ph);
@@ -776,13 +891,23 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
         } else if (R > 1) {
           there[0] = there[R - 1];
         }
+        // The largest scale so far and the least of this tile decide its form.
+        ok = pf_wait(sh, sh.ranges + (j & 1), j >> 1 & 1);
+        if (!__all_sync(0xffffffffu, ok)) break;
+#pragma unroll
+        for (int w = 0; w < kPfWiden; ++w) {
+          const uint2 r = sh.range[j & 1][w];
+          top_e = max(top_e, r.x);
+          least = min(least, r.y);
+        }
+        const bool far = least + kPfSpread < top_e;
         // what softmax needs to know of the tile, in the place of j - 2's:
         // O(j - 2) is done
         if (R == 2 && j >= 2) {
           ok = pf_wait_ring(sh, sh.v_free, j - R);
           if (!__all_sync(0xffffffffu, ok)) break;
         }
-        // factor: 2^(e - E), exact down to 2^-24 and zero below
+        // factor: 2^(e - E), 2^-8 or more (in a far tile it is not used)
         uint32_t factor[kPfOwn / 2];
 #pragma unroll
         for (int i = 0; i < kPfOwn / 2; ++i) {
@@ -797,10 +922,12 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
           }
           sh.k_scale[j & 1][kPage * pg + (lane & 15)] =
               __uint_as_float(ke[i] << 23);
+          if (far) sh.v_token[j & 1][kPage * pg + (lane & 15)] = (uint8_t)ve[i];
           factor[i] = h2_as_u32(
               __float2half2_rn(exp2_int(max(-126, (int)ve[i] - (int)top))));
         }
         if (lane == 0) sh.there[j & 1][own] = now << first;
+        if (lane == 0 && own == 0) sh.far[j & 1] = far;
         __syncwarp();
         if (lane == 0) mbar_arrive(sh.info + (j & 1));
         // O(j - 1) done: its values may go
@@ -809,24 +936,35 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
           if (!__all_sync(0xffffffffu, ok)) break;
         }
         const uint32_t to = v_s + j % R * 2 * kPfBlock;
+        auto widen = [&](auto number) {
 #pragma unroll
-        for (int u = 0; u < 4 * kPfOwn; ++u) {
-          const int sl = 4 * (u & 3) + s4;
-          const __half2 x = u32_as_h2(__shfl_sync(
-              0xffffffffu, factor[u >> 3], 16 * (u >> 2 & 1) + sl));
-          const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
-          uint32_t y[8];
+          for (int u = 0; u < 4 * kPfOwn; ++u) {
+            const int sl = 4 * (u & 3) + s4;
+            const __half2 x = u32_as_h2(__shfl_sync(
+                0xffffffffu, factor[u >> 3], 16 * (u >> 2 & 1) + sl));
+            const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+            uint32_t y[8];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            y[2 * k] = h2_as_u32(__hmul2(u32_as_h2(e4m3x2_lo(w[k])), x));
-            y[2 * k + 1] = h2_as_u32(__hmul2(u32_as_h2(e4m3x2_hi(w[k])), x));
+            for (int k = 0; k < 4; ++k) {
+              y[2 * k] = number(u32_as_h2(e4m3x2_lo(w[k])), x);
+              y[2 * k + 1] = number(u32_as_h2(e4m3x2_hi(w[k])), x);
+            }
+            const int r = (first + (u >> 2)) * kPage + sl;
+            st_shared_v4(to + tile_at(r, 2 * c),
+                         make_uint4(y[0], y[1], y[2], y[3]));
+            st_shared_v4(to + tile_at(r, 2 * c + 1),
+                         make_uint4(y[4], y[5], y[6], y[7]));
           }
-          const int r = (first + (u >> 2)) * kPage + sl;
-          st_shared_v4(to + tile_at(r, 2 * c),
-                       make_uint4(y[0], y[1], y[2], y[3]));
-          st_shared_v4(to + tile_at(r, 2 * c + 1),
-                       make_uint4(y[4], y[5], y[6], y[7]));
-        }
+        };
+        if (far)  // the codes themselves
+          widen([](__half2 code, __half2) -> uint32_t {
+            const __nv_bfloat162 y = __float22bfloat162_rn(__half22float2(code));
+            return *reinterpret_cast<const uint32_t *>(&y);
+          });
+        else
+          widen([](__half2 code, __half2 x) -> uint32_t {
+            return h2_as_u32(__hmul2(code, x));
+          });
         fence_to_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(sh.v_full + j % R);
