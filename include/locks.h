@@ -583,9 +583,9 @@ locks_status_t locks_quantised_decode(
  *   workspace     >= locks_prefix_workspace_size bytes, its first int32 the
  *                 device status word, as for the other calls
  * Other arguments and errors as locks_quantised_decode, and so the weights; the
- * query of the shared pages takes part as the sum of two e4m3 numbers, off by
- * at most 2^-18 of its head's largest element where it is 2^-11 of that or
- * less. */
+ * query of the shared pages takes part as the sum of two 8-bit numbers, exact
+ * but for elements below 2^-13 of their head's largest, which are off by at
+ * most 2^-21 of that. */
 locks_status_t locks_prefix_decode(
     const void *q, const void *records, int64_t num_phys_pages,
     const int32_t *prefix_table, int prefix_pages, const int32_t *page_table,

@@ -9,11 +9,14 @@
 // fp16 in tensor memory over the scores they came from.
 //
 // Keys take part as they are stored: the e4m3 rows are copied to shared
-// memory, and the query row is the sum of two e4m3 rows, hi + lo, after a
-// power-of-two scale that puts its largest magnitude in (224, 448].  A bf16
-// number has 8 significant bits, a code 4, so hi + lo is exact down to 2^-11
-// of the row's largest element and off by at most 2^-10, 2^-18 of it, below.
-// A key's scale multiplies its column of scores.  Value codes are widened to
+// memory, and the query row is the sum of two rows of codes, hi in e4m3 and lo
+// in e5m2, after a power-of-two scale that puts its largest magnitude in (224,
+// 448].  A bf16 number has 8 significant bits.  hi, of 4, leaves a rest of at
+// most 8 of its last places, which lo's 3 bits hold (a rest of 9 to 15 would
+// take 4), so that hi + lo is exact from 2^-6 on, 2^-13 of the row's largest
+// element.  Below, hi's step is 2^-9 and lo, whose own goes down to 2^-16, is
+// off by at most 2^-14, 2^-21 of the row's largest element: what fp32 products
+// with that element lose.  (Both in e4m3, it was 2^-17.)  A key's scale multiplies its column of scores.  Value codes are widened to
 // fp16, a page's rows scaled by 2^(e - E), E the largest exponent of the
 // page, which joins the weights' exponent: exact, since a tile with rows more
 // than 2^8 below the largest scale so far takes another form (far_tile: codes
@@ -105,6 +108,8 @@ __device__ __forceinline__ uint64_t mat_desc(uint32_t addr, uint32_t lead) {
 // kind::f16), M = 128, N = a tile's tokens or the dims; bit 16: B runs along N
 constexpr uint32_t kPfDescS =
     1u << 4 | ((uint32_t)kPfTile >> 3) << 17 | (128u >> 4) << 24;
+// .. A in e5m2, the query's lo
+constexpr uint32_t kPfDescLo = kPfDescS | 1u << 7;
 constexpr uint32_t kPfDescO =
     1u << 4 | 1u << 16 | ((uint32_t)kDim >> 3) << 17 | (128u >> 4) << 24;
 // .. both operands bf16
@@ -221,6 +226,15 @@ __device__ __forceinline__ void st_shared_v4(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(a), "r"(v.x),
                "r"(v.y), "r"(v.z), "r"(v.w)
                : "memory");
+}
+
+// two numbers -> two e5m2 codes (low byte: lo), as e4m3x2_from
+__device__ __forceinline__ uint32_t e5m2x2_from(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;\n"
+      : "=h"(r)
+      : "f"(hi), "f"(lo));
+  return r;
 }
 
 // two fp32 numbers in one 64-bit register pair
@@ -454,8 +468,8 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
           const float2 h0 = __half22float2(u32_as_h2(e4m3x2_lo(c)));
           const float2 h1 = __half22float2(u32_as_h2(e4m3x2_hi(c)));
           hi[2 * k + n2] = c;
-          lo[2 * k + n2] = e4m3x2_from(a0 - h0.x, a1 - h0.y) |
-                           e4m3x2_from(a2 - h1.x, a3 - h1.y) << 16;
+          lo[2 * k + n2] = e5m2x2_from(a0 - h0.x, a1 - h0.y) |
+                           e5m2x2_from(a2 - h1.x, a3 - h1.y) << 16;
         }
       }
       const uint32_t at = q_s + tile * 2 * kPfQuery + (tid & 127) * 128 +
@@ -712,7 +726,7 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
           for (int kk = 0; kk < 8; ++kk)  // hi, then lo
             mma_ss(tm + t * kPfColumns,
                    q + ((kk >> 2) * (kPfQuery >> 4) + (kk & 3) * 2),
-                   k + (kk & 3) * 2, kPfDescS, kk > 0);
+                   k + (kk & 3) * 2, kk < 4 ? kPfDescS : kPfDescLo, kk > 0);
           mma_commit(sh.qk_done + t);
           if (t == nt - 1) mma_commit(sh.k_free + j % R);
         }

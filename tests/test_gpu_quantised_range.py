@@ -143,8 +143,8 @@ def test_steps_back_to_back_see_the_latest_inputs(batch, np_):
 #   * scores off by dx each: a weight by expm1(2 max dx) of it, the largest
 #     weight by as much of all the others'
 #   * dx: 128 products and sums, 2^-24 each; fp32 exponents of numbers up to
-#     |x| + 64, twice; the query as the call takes it (`query`: its step, as a
-#     share of the row's largest element)
+#     |x| + 64, twice; the query as the call takes it (`query`: an element's
+#     error, as a share of the row's largest, or of each element by itself)
 #   * lse: max dx, fp32 rounding
 # Outputs in dims where the far larger rows hold zeros are sums of the others
 # alone, so these hold element by element, not against the row's largest.
@@ -154,8 +154,9 @@ def bounds(q, K, V, query):
         return (np.zeros((G, 128)), np.full(G, -np.inf), np.zeros((G, 128)),
                 np.zeros(G))
     x = q @ K.T / math.sqrt(128)
-    dx = (2.0 ** -17 * np.abs(q) @ np.abs(K).T + query *
-          np.abs(q).max(1, keepdims=True) * np.abs(K).sum(1)) / math.sqrt(128)
+    off = query(q) if callable(query) else np.broadcast_to(
+        query * np.abs(q).max(1, keepdims=True), q.shape)
+    dx = (2.0 ** -17 * np.abs(q) + off) @ np.abs(K).T / math.sqrt(128)
     dx = (dx + 2.0 ** -22 * (np.abs(x) + 64)).max(1)
     top = x.max(1, keepdims=True)
     w = np.exp(x - top)
@@ -414,3 +415,46 @@ def test_shared_values_of_the_whole_scale_range(batch, G, h_kv, np_):
     rec[prefix] = part
     expect(run_shared(q, rec, tables, lens, prefix), qn, rec, tables, lens,
            prefix=prefix, query=2.0 ** -18)
+
+
+# ---------------------------------------------------------------------------
+# queries with an outlier
+# ---------------------------------------------------------------------------
+def shared_query_error(q):
+    """hi + lo of the shared pages' query: scaled by a power of two that puts
+    the row's largest in (224, 448], off by 2^-14 at most below 2^-6."""
+    unit = 2.0 ** np.ceil(np.log2(np.abs(q).max(1, keepdims=True) / 448))
+    return np.where(np.abs(q) < 2.0 ** -6 * unit, 2.0 ** -14 * unit, 0.0)
+
+
+@pytest.mark.parametrize("batch,G,h_kv,np_", SHARED)
+@pytest.mark.parametrize("ratio", [30, 1000, 20000])
+@pytest.mark.parametrize("keys", ["alike", "apart"])
+def test_shared_query_with_an_outlier_channel(batch, G, h_kv, np_, ratio,
+                                              keys):
+    # one element far above the rest, against keys that are small there: the
+    # other elements carry the score.  With all keys alike a score's error
+    # does not average out of the log-sum-exp
+    rng = np.random.default_rng(ratio)
+    rec, tables, prefix, lens, q, qn = shared_case(rng, batch, G, h_kv, np_,
+                                                   -9)
+    q[:, :, 40] *= ratio
+    if keys == "apart":       # some tokens well above the others
+        q *= 3
+    qn = q.double().numpy()
+    for h in range(h_kv):
+        k = rng.standard_normal((64, 128))
+        k[:, 40] /= ratio
+        codes, e = Q.quantise_rows(k)
+        at = np.zeros(rec.shape[0] * 16, np.int64)
+        if keys == "apart":
+            at = rng.integers(0, 64, at.shape)
+        part = np.empty((at.size, 128), np.uint8)
+        part[:] = codes[at]
+        place = np.array(Q._PLACE).reshape(-1)
+        rows = np.empty((rec.shape[0], 2048), np.uint8)
+        rows[:, place] = part.reshape(rec.shape[0], 2048)
+        rec[:, h, :2048] = rows
+        rec[:, h, 4096:4112] = (127 + e[at]).reshape(-1, 16)
+    expect(run_shared(q, rec, tables, lens, prefix), qn, rec, tables, lens,
+           prefix=prefix, query=shared_query_error)
