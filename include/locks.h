@@ -503,6 +503,8 @@ void locks_decoder_destroy(locks_decoder_t *decoder);
  * become +-448 * 2^31; NaN stays NaN and has no part in the maximum; rows
  * below 448 * 2^-32 keep e = -32 and lose low bits.  A number read back,
  * code * 2^e, is exact in bf16 and fp32.
+ * Records of zeros, as of a new cache, read as rows of zeros, and take part in
+ * attention as such where a length covers them.
  * ------------------------------------------------------------------------ */
 
 /* Write rows of new tokens (a prompt's, or one per sequence) into the

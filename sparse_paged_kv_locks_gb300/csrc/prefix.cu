@@ -870,6 +870,7 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
           asm volatile("ld.shared.u8 %0, [%1];\n"
                        : "=r"(ve[i])
                        : "r"(at + (kQOffVE - kQOffV)));
+          ve[i] = q_scale_byte(ve[i]);
         }
         // The largest and the least scale of these pages, for both warps.  (The
         // place of j - 2: the other warp has read it, or it had not come to the

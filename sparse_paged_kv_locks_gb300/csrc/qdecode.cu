@@ -495,6 +495,7 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       ks[r] = __uint_as_float(ek[r] << 23);
+      e2[r] = q_scale_byte(e2[r]);
       ev[r] = (float)((int)e2[r] - 127);
       vi[r] = __uint_as_float((254u - e2[r]) << 23);
     }

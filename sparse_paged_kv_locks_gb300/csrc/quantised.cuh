@@ -42,6 +42,14 @@ __device__ __forceinline__ int q_exponent(float absmax) {
   return max(kQExpLo, min(kQExpHi, e));
 }
 
+// A value scale's byte as the attention takes it.  Zeroed records, which no row
+// has been written to, hold 0 there: codes of zero, so that any scale stands
+// for the same values, and one of the format's keeps the sums of weights times
+// 2^-e in range.
+__device__ __forceinline__ uint32_t q_scale_byte(uint32_t b) {
+  return max(b, (uint32_t)(kQExpLo + 127));
+}
+
 __device__ __forceinline__ float exp2_int(int e) {  // 2^e, -126 <= e <= 127
   return __uint_as_float((uint32_t)(e + 127) << 23);
 }

@@ -458,3 +458,38 @@ def test_shared_query_with_an_outlier_channel(batch, G, h_kv, np_, ratio,
         rec[:, h, 4096:4112] = (127 + e[at]).reshape(-1, 16)
     expect(run_shared(q, rec, tables, lens, prefix), qn, rec, tables, lens,
            prefix=prefix, query=shared_query_error)
+
+
+# ---------------------------------------------------------------------------
+# records never written
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("centre", [-9, 4, 25])
+@pytest.mark.parametrize("G,room", [(4, 0), (4, 600), (12, 0)])
+def test_zeroed_records_inside_a_length(centre, G, room):
+    # a new cache is zeros, scale bytes too: keys and values of zero, which
+    # have their share of the weights whatever the other rows' scales
+    rng = np.random.default_rng(centre + 9)
+    lens = [300, 80, 45]
+    rec, tables, _ = layout(rng, lens, 2, centre, room)
+    for b, pages in ((0, [1, 4, 5, 18]), (1, [0]), (2, [0, 1])):
+        rec[tables[b, pages]] = 0
+    q = normal(rng, 3, 2 * G, 128)
+    expect(run_lists(q, rec, tables, lens), q.double().numpy(), rec, tables,
+           lens)
+
+
+@pytest.mark.parametrize("batch,G,h_kv,np_", SHARED)
+@pytest.mark.parametrize("centre", [-9, 4, 25])
+def test_shared_zeroed_records(batch, G, h_kv, np_, centre):
+    rng = np.random.default_rng(np_)
+    rec, tables, prefix, lens, q, qn = shared_case(rng, batch, G, h_kv, np_,
+                                                   centre)
+    rec[prefix[rng.random(np_) < 0.3]] = 0
+    rec[prefix[16:40]] = 0             # whole tiles
+    for b in (0, 5):                   # single rows
+        for s in range(b, 16, 3):
+            r = rec[prefix[7 + b]]
+            r[:, Q._PLACE[s]] = r[:, 2048 + Q._PLACE[s]] = 0
+            r[:, [4096 + s, 4112 + s]] = 0
+    expect(run_shared(q, rec, tables, lens, prefix), qn, rec, tables, lens,
+           prefix=prefix, query=shared_query_error)
