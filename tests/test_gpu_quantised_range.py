@@ -493,3 +493,123 @@ def test_shared_zeroed_records(batch, G, h_kv, np_, centre):
             r[:, [4096 + s, 4112 + s]] = 0
     expect(run_shared(q, rec, tables, lens, prefix), qn, rec, tables, lens,
            prefix=prefix, query=shared_query_error)
+
+
+# ---------------------------------------------------------------------------
+# scores that rise, extreme queries
+# ---------------------------------------------------------------------------
+def kernel_names(call):
+    from torch.profiler import ProfilerActivity, profile
+    for _ in range(2):       # a process's first profile may come back empty
+        torch.cuda.synchronize()
+        with profile(activities=[ProfilerActivity.CUDA]) as p:
+            call()
+            torch.cuda.synchronize()
+        names = " ".join(e.key for e in p.key_averages())
+        if names:
+            return names
+    pytest.skip("no kernel names from the profiler")
+
+
+@pytest.mark.parametrize("batch,G,h_kv,np_,tiles", [
+    (2, 8, 8, 1543, 1), (67, 16, 2, 905, 2)])
+def test_shared_forms(batch, G, h_kv, np_, tiles):
+    # the cases below mean these forms of the kernel, chosen by sizes: one or
+    # two tiles of query rows to a CTA, and at least two tiles of tokens to a
+    # range (there are at most 608 CTAs with one, 304 with two)
+    rng = np.random.default_rng(0)
+    rec, tables, prefix, lens, q, _ = shared_case(rng, max(batch, 4), G, h_kv,
+                                                  np_, -9)
+    names = kernel_names(lambda: run_shared(q[:batch], rec, tables[:batch],
+                                            lens[:batch], prefix))
+    assert f"prefix_kernel<{tiles}>" in names
+    row_tiles = -(-batch * G // 128)
+    ranges = 608 // tiles / (-(-row_tiles // tiles) * h_kv)
+    assert -(-np_ // 8) >= 2 * ranges
+
+
+def rising_keys(rng, rec, pages, q_unit, levels):
+    """Keys of page i of `pages` along q_unit [128], scoring levels[i] with
+    it."""
+    for i, pg in enumerate(pages):
+        for s in range(16):
+            x = levels[i][s] * math.sqrt(128) / (q_unit ** 2).sum()
+            # the spread keeps the rounding of the codes from adding up
+            k = x * q_unit * (1 + 0.1 * rng.uniform(-1, 1, (rec.shape[1], 128)))
+            codes, e = Q.quantise_rows(k)
+            for h in range(rec.shape[1]):
+                rec[pg, h, Q._PLACE[s]] = codes[h]
+                rec[pg, h, 4096 + s] = 127 + e[h]
+
+
+@pytest.mark.parametrize("batch,G,h_kv,np_", [(6, 5, 8, 515), (2, 8, 8, 1543),
+                                              (67, 16, 2, 905)])
+@pytest.mark.parametrize("spread", [2, 14])
+def test_shared_scores_that_rise(batch, G, h_kv, np_, spread):
+    # along the tiles of a range and in the middle of a tile, for rows of
+    # different steepness: sums and weights are rescaled again and again, in
+    # tiles of either form (value scales near one another, and far apart)
+    rng = np.random.default_rng(np_ + spread)
+    lens = [16 * np_ + int(n) for n in rng.integers(0, 40, batch)]
+    rec, tables, prefix = layout(rng, lens, h_kv, -9, np_=np_)
+    if spread > 2:
+        part = rec[prefix]
+        part[..., 4112:] = 127 + rng.integers(-spread, spread + 1,
+                                              part[..., 4112:].shape)
+        rec[prefix] = part
+    unit = rng.choice([-1.0, 1.0], 128)
+    steep = rng.choice([0.5, 1.0, 1.5, 2.0], (batch, h_kv * G, 1))
+    q = torch.from_numpy(steep * unit + 0.05 * rng.standard_normal(
+        (batch, h_kv * G, 128))).to(torch.bfloat16)
+    page = np.arange(np_)
+    levels = 5.0 * (page // 8 % 8) + 6.0 * (page // 4 % 2) - 20
+    rising_keys(rng, rec, prefix, unit,
+                levels[:, None] + rng.uniform(-1, 1, (np_, 16)))
+    expect(run_shared(q, rec, tables, lens, prefix), q.double().numpy(), rec,
+           tables, lens, prefix=prefix, query=shared_query_error)
+
+
+@pytest.mark.parametrize("lens,h_kv,room,k", FORMS)
+@pytest.mark.parametrize("spread", [2, 14])
+def test_scores_that_rise(lens, h_kv, room, k, spread):
+    rng = np.random.default_rng(spread)
+    rec, tables, _ = layout(rng, lens, h_kv, -9, room)
+    live = rec[..., 4112:] < 255
+    if spread > 2:
+        rec[..., 4112:] = np.where(
+            live, 127 + rng.integers(-spread, spread + 1, live.shape), 255)
+    unit = rng.choice([-1.0, 1.0], 128)
+    for b, n in enumerate(lens):
+        full = tables[b, :n // 16]
+        levels = 5.0 * (np.arange(len(full)) % 8) - 20
+        rising_keys(rng, rec, full, unit,
+                    levels[:, None] + rng.uniform(-1, 1, (len(full), 16)))
+    steep = rng.choice([0.5, 1.0, 1.5, 2.0], (len(lens), h_kv * 4, 1))
+    q = torch.from_numpy(steep * unit + 0.05 * rng.standard_normal(
+        (len(lens), h_kv * 4, 128))).to(torch.bfloat16)
+    idx = lists(rng, lens, h_kv, k) if k else None
+    expect(run_lists(q, rec, tables, lens, idx), q.double().numpy(), rec,
+           tables, lens, idx)
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e-3, 30.0, 1e3, 1e6])
+@pytest.mark.parametrize("form", [0, 1, 2, "shared"])
+def test_queries_of_any_size(scale, form):
+    # every output against the definition: at the largest sizes one token
+    # takes a row, and which one does not depend on the scores' last bits
+    rng = np.random.default_rng(8)
+    if form == "shared":
+        rec, tables, prefix, lens, q, _ = shared_case(rng, *SHARED[1], -9)
+    else:
+        lens, h_kv, room, k = FORMS[form]
+        rec, tables, _ = layout(rng, lens, h_kv, -9, room)
+        q = normal(rng, len(lens), 4 * h_kv, 128)
+    q = (scale * q.double()).to(torch.bfloat16)
+    qn = q.double().numpy()
+    if form == "shared":
+        expect(run_shared(q, rec, tables, lens, prefix), qn, rec, tables, lens,
+               prefix=prefix, query=shared_query_error)
+    else:
+        idx = lists(rng, lens, h_kv, k) if k else None
+        expect(run_lists(q, rec, tables, lens, idx), qn, rec, tables, lens,
+               idx)
