@@ -16,7 +16,9 @@
 // take 4), so that hi + lo is exact from 2^-6 on, 2^-13 of the row's largest
 // element.  Below, hi's step is 2^-9 and lo, whose own goes down to 2^-16, is
 // off by at most 2^-14, 2^-21 of the row's largest element: what fp32 products
-// with that element lose.  (Both in e4m3, it was 2^-17.)  A key's scale multiplies its column of scores.  Value codes are widened to
+// with that element lose.  (Both in e4m3, it was 2^-17.)
+//
+// A key's scale multiplies its column of scores.  Value codes are widened to
 // fp16, a page's rows scaled by 2^(e - E), E the largest exponent of the
 // page, which joins the weights' exponent: exact, since a tile with rows more
 // than 2^8 below the largest scale so far takes another form (far_tile: codes
@@ -81,17 +83,13 @@ template <int R>
 constexpr int kPfThreads = 32 * (4 * R + 2 + kPfWiden);
 template <int R>
 constexpr int kPfSmem = R * kPfPart + 1024;
-constexpr float kPfScale = 0.12751743074602467f;  // log2(e) / sqrt(128)
 // fewest (sequence, KV head, page) triples that are worth the kernel
 constexpr long long kPfMinShared = 12288;
-constexpr float kPfLift = 8.f;   // as in the single-token kernel
-constexpr float kPfSlack = 7.f;
-// A tile with value rows more than 2^8 below the largest scale so far takes its
-// weights and values in bf16 (far_tile).  Twice the time, for tiles after an
-// outlier's alone: with an infinity in its first page a 128K prefix for 64
-// sequences takes 620 us instead of 276 (the range that holds it is the last to
-// end), one of 32K for 32 49 us instead of 47.
-constexpr uint32_t kPfSpread = 8;
+// A tile with value rows more than 2^kQSpread below the largest scale so far
+// takes its weights and values in bf16 (far_tile).  Twice the time, for tiles
+// after an outlier's alone: with an infinity in its first page a 128K prefix for
+// 64 sequences takes 620 us instead of 276 (the range that holds it is the last
+// to end), one of 32K for 32 49 us instead of 47.
 
 // ---------------------------------------------------------------------------
 // tcgen05
@@ -272,16 +270,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// bytes from global memory to shared address `to`
-__device__ __forceinline__ void bulk_rows(uint32_t to, const void *from,
-                                          uint32_t bytes, uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes "
-      "[%0], [%1], %2, [%3];\n" ::"r"(to),
-      "l"(from), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
-}
-
 // byte offset of 16-byte chunk c (0..15, 8 fp16 each) of row r in a tile:
 // two blocks of 64 dims, rows of 128 bytes, chunks swizzled by the row
 __device__ __forceinline__ uint32_t tile_at(int r, int c) {
@@ -448,7 +436,7 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
     const float down = exp2_int(-e);
     // codes have no infinity: a row that holds one has scores that are not
     // numbers
-    const float f = isinf(top) ? top - top : exp2_int(e) * kPfScale;
+    const float f = isinf(top) ? top - top : exp2_int(e) * kQScale;
 #pragma unroll 2
     for (int i = 0; i < 8; ++i) {  // 16 dims
       uint32_t hi[4], lo[4];
@@ -525,7 +513,7 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
             top = fmaxf(top, score(s[i], kPage * pg + i, scale(e, i)));
         }
       }
-      const bool raise = top > m + kPfSlack;
+      const bool raise = top > m + kQSlack;
       if (__any_sync(0xffffffffu, raise)) {
         const float to = raise ? top : m;
         const float fall = to == m ? 1.f : ex2_fast(m - to);
@@ -548,7 +536,7 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
             const int t = 2 * i + k;
             const uint32_t ev = scale(e, t);
             u[k] = here ? ex2_fast(score(s[t], kPage * pg + t, ev) -
-                                   (m - kPfLift))
+                                   (m - kQLift))
                         : 0.f;
             if (here) l = fmaf(u[k], __uint_as_float((254u - ev) << 23), l);
           }
@@ -608,7 +596,7 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
           if (there >> pg & 1)
             top = fmaxf(top, fmaf(t1, f, sh.v_exp[par][pg]));
         }
-        const bool raise = top > m + kPfSlack;
+        const bool raise = top > m + kQSlack;
         if (__any_sync(0xffffffffu, raise)) {  // rare after the first tiles
           const float to = raise ? top : m;
           const float fall = to == m ? 1.f : ex2_fast(m - to);
@@ -633,7 +621,7 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
           const int pg = 4 * c + p;
-          const float add = sh.v_exp[par][pg] - (m - kPfLift);
+          const float add = sh.v_exp[par][pg] - (m - kQLift);
           const uint64_t aa = pack2(add, add);
           uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -706,9 +694,9 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
       if (lane == 0) mbar_arrive_tx(bar, __popc(there) * bytes);
       __syncwarp();
       if (here)
-        bulk_rows(to + lane * bytes,
-                  a.records + ((size_t)ph * a.h_kv + h) * kQRec + off, bytes,
-                  bar);
+        bulk_g2s(to + lane * bytes,
+                 a.records + ((size_t)ph * a.h_kv + h) * kQRec + off, bytes,
+                 bar);
       __syncwarp();
       return there;
     };
@@ -863,7 +851,8 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
         uint32_t ke[kPfOwn / 2], ve[kPfOwn / 2];
 #pragma unroll
         for (int i = 0; i < kPfOwn / 2; ++i) {
-          const uint32_t at = from + (2 * i + (lane >> 4)) * kPfRest + (lane & 15);
+          const uint32_t at =
+              from + (2 * i + (lane >> 4)) * kPfRest + (lane & 15);
           asm volatile("ld.shared.u8 %0, [%1];\n"
                        : "=r"(ke[i])
                        : "r"(at + (kQOffKE - kQOffV)));
@@ -915,7 +904,7 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
           top_e = max(top_e, r.x);
           least = min(least, r.y);
         }
-        const bool far = least + kPfSpread < top_e;
+        const bool far = least + kQSpread < top_e;
         // what softmax needs to know of the tile, in the place of j - 2's:
         // O(j - 2) is done
         if (R == 2 && j >= 2) {
@@ -973,7 +962,8 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
         };
         if (far)  // the codes themselves
           widen([](__half2 code, __half2) -> uint32_t {
-            const __nv_bfloat162 y = __float22bfloat162_rn(__half22float2(code));
+            const __nv_bfloat162 y =
+                __float22bfloat162_rn(__half22float2(code));
             return *reinterpret_cast<const uint32_t *>(&y);
           });
         else
@@ -1027,12 +1017,17 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
 //
 // 0 ranges: too little to share, every sequence reads the pages itself.
 // (Sequences, KV heads, pages, G = 4 unless given: read by each against once,
-// us.)  8, 8, 128: 13 and 17; 8, 8, 256: 24 and 18; 2, 8, 256: 14 and 17; 2, 8,
-// 1024: 25 and 24; 2, 8, 2048: 33 and 32; 32, 8, 32: 12 and 19; 32, 8, 64: 25
-// and 20; 64, 8, 16, G = 8: 18 and 21; 64, 8, 32, G = 8: 21 and 23; 64, 8, 64,
-// G = 8: 33 and 24; 16, 8, 64, G = 16: 17 and 24; 16, 8, 128, G = 16: 31 and 25;
-// 256, 8, 4, G = 1: 25 and 21; 256, 8, 8, G = 1: 29 and 21; 128, 1, 64, G = 8:
-// 14 and 19; 128, 1, 128, G = 8: 27 and 22; one sequence, 8, 8192: 64 and 77.
+// us, replayed back to back.)
+//   triples below the limit: 8, 8, 128: 12.4 and 13.6; 2, 8, 256: 10.9 and 13.7;
+//     32, 8, 32: 11.4 and 16.1; 64, 8, 16, G = 8: 15.6 and 18.3; 16, 8, 64,
+//     G = 16: 14.0 and 21.7; 128, 1, 64, G = 8: 12.9 and 16.9; but 256, 8, 4,
+//     G = 1: 23.3 and 18.0
+//   above: 8, 8, 256: 21.1 and 15.0; 2, 8, 1024: 21.0 and 20.4; 2, 8, 2048: 29.2
+//     and 27.8; 32, 8, 64: 23.0 and 16.6; 64, 8, 32, G = 8: 19.9 and 20.2; 64,
+//     8, 64, G = 8: 31.4 and 21.0; 16, 8, 128, G = 16: 28.3 and 22.7; 256, 8, 8,
+//     G = 1: 26.9 and 17.8; 128, 1, 128, G = 8: 24.2 and 18.0
+// One sequence shares nothing (1, 8, 8192: 64 and 77).  The numbers of SMs and
+// of CTAs that fit on them are this GPU's, written out.
 PrefixPlan prefix_plan(int batch, int h_kv, int G, int pages) {
   PrefixPlan plan{0, false};
   if (batch < 2 || (long long)batch * h_kv * pages < kPfMinShared) return plan;

@@ -25,9 +25,11 @@
 // 24.5 us, this kernel without its arithmetic 29 us: what is left is the
 // look-ups before the first copy and the merge after the last.  Two units of
 // warps and stages were tried, 4 x 4 at three CTAs an SM and 8 x 3 at two: the
-// same for lists, 72 against 92 us for a dense ragged batch.  Tokens (then dims) are the M dimension of
-// mma.m16n8k16 and the query heads the N dimension: a group of up to 8 heads
-// is one column tile, and the page's 16 tokens fill M.  The order of dims in
+// same for lists, 72 against 92 us for a dense ragged batch.
+//
+// Tokens (then dims) are the M dimension of mma.m16n8k16 and the query heads
+// the N dimension: a group of up to 8 heads is one column tile, and the page's
+// 16 tokens fill M.  The order of dims in
 // the products is free, so a lane's A fragments are whole 16-byte groups of a
 // key row, and for the second product the 16 dims of one group.
 #include "launch.h"
@@ -50,16 +52,12 @@ constexpr int kQdMinRun = 12, kQdMinRunBeside = 2;
 // unit form for lists that are not given: tables of at most this many pages
 // per CTA (a short sequence leaves its CTA idle, a long one would keep it)
 constexpr int kQdUnitPages = 64;
-constexpr float kQdScale = 0.12751743074602467f;  // log2(e) / sqrt(128)
 constexpr float kQdLn2 = 0.69314718055994531f;
-constexpr float kQdLift = 8.f;    // weights are 2^(.. - m + 8)
-constexpr float kQdSlack = 7.f;   // .. and m trails the maximum by at most 7
 // Weights below fp16's normal numbers, of rows whose value scale is more than
-// 2^8 below the largest of the pages that raised m, are taken in bins of 24
-// powers of two each.  Ordinary pages pay two comparisons; with an infinity in
+// 2^kQSpread below the largest of the pages that raised m, are taken in bins of
+// 24 powers of two each.  Ordinary pages pay two comparisons; with an infinity in
 // every sequence's first page, 256 lists of 128 pages take 43 us instead of 30
 // and a dense ragged batch 80 instead of 70.
-constexpr uint32_t kQdSpread = 8;
 constexpr float kQdNormal = -14.f, kQdBin = 24.f;
 constexpr int kQdBins = 4;
 
@@ -144,10 +142,6 @@ __device__ __forceinline__ QEntry q_resolve(const QdArgs &a,
 
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   return h2_as_u32(__floats2half2_rn(lo, hi));
-}
-__device__ __forceinline__ uint32_t byte_perm(uint32_t a, uint32_t b,
-                                              uint32_t sel) {
-  return __byte_perm(a, b, sel);
 }
 __device__ __forceinline__ uint32_t pack_bf2q(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -306,7 +300,7 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
       for (int i = 0; i < 16; ++i)
         qb[nt][i >> 1][i & 1] =
             pack_h2(bf16_lo(raw[i]) * down, bf16_hi(raw[i]) * down);
-      const float fe = exp2_int(e) * kQdScale;
+      const float fe = exp2_int(e) * kQScale;
       f[nt][0] = __shfl_sync(0xffffffffu, fe, 8 * t);
       f[nt][1] = __shfl_sync(0xffffffffu, fe, 8 * t + 4);
     }
@@ -362,7 +356,7 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
           if (g == 0)
             a.lse_out[row] = ls == 0.f
                                  ? -INFINITY
-                                 : (log2f(ls) + (m[nt][c] - kQdLift)) * kQdLn2;
+                                 : (log2f(ls) + (m[nt][c] - kQLift)) * kQdLn2;
         } else {
           float *po = UNIT ? reinterpret_cast<float *>(ring) + hd * kDim
                            : a.o_part + (((size_t)u + gw) * a.G + hd) * kDim;
@@ -419,7 +413,7 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
         float w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float y = z[nt][i] - (m[nt][i & 1] - kQdLift) + up;
+          const float y = z[nt][i] - (m[nt][i & 1] - kQLift) + up;
           const bool here = y >= kQdNormal && y < kQdNormal + kQdBin;
           w[i] = here ? ex2_fast(y) : 0.f;
           some |= here;
@@ -433,10 +427,10 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
                      *v3 = &vc[3].x;
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const uint32_t a01 = byte_perm(v0[w], v1[w], 0x5140);
-        const uint32_t a23 = byte_perm(v2[w], v3[w], 0x5140);
-        const uint32_t b01 = byte_perm(v0[w], v1[w], 0x7362);
-        const uint32_t b23 = byte_perm(v2[w], v3[w], 0x7362);
+        const uint32_t a01 = __byte_perm(v0[w], v1[w], 0x5140);
+        const uint32_t a23 = __byte_perm(v2[w], v3[w], 0x5140);
+        const uint32_t b01 = __byte_perm(v0[w], v1[w], 0x7362);
+        const uint32_t b23 = __byte_perm(v2[w], v3[w], 0x7362);
         const uint32_t fa[4] = {e4m3x2_lo(a01), e4m3x2_hi(a01), e4m3x2_lo(a23),
                                 e4m3x2_hi(a23)};
         const uint32_t fb[4] = {e4m3x2_lo(b01), e4m3x2_hi(b01), e4m3x2_lo(b23),
@@ -534,8 +528,8 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
     // weights
     const bool in0 = g < ntok, in1 = g + 8 < ntok;
     float z[NT][4];
-    const bool far0 = in0 && e2[0] + kQdSpread < e_top;
-    const bool far1 = in1 && e2[1] + kQdSpread < e_top;
+    const bool far0 = in0 && e2[0] + kQSpread < e_top;
+    const bool far1 = in1 && e2[1] + kQSpread < e_top;
     bool raise = far0 || far1, binned = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -544,7 +538,7 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
         z[nt][c] = in0 ? fmaf(s[nt][c], f[nt][c] * ks[0], ev[0]) : -INFINITY;
         z[nt][2 + c] =
             in1 ? fmaf(s[nt][2 + c], f[nt][c] * ks[1], ev[1]) : -INFINITY;
-        raise |= fmaxf(z[nt][c], z[nt][2 + c]) > m[nt][c] + kQdSlack;
+        raise |= fmaxf(z[nt][c], z[nt][2 + c]) > m[nt][c] + kQSlack;
       }
     if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -576,9 +570,9 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const float least = m[nt][c] - kQdLift + kQdNormal;
-          low |= in0 && e2[0] + kQdSpread < e_top && z[nt][c] < least;
-          low |= in1 && e2[1] + kQdSpread < e_top && z[nt][2 + c] < least;
+          const float least = m[nt][c] - kQLift + kQdNormal;
+          low |= in0 && e2[0] + kQSpread < e_top && z[nt][c] < least;
+          low |= in1 && e2[1] + kQSpread < e_top && z[nt][2 + c] < least;
         }
       binned = __any_sync(0xffffffffu, low);
       if (binned) binned_weights(z, vc);
@@ -589,7 +583,7 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
       float w[4];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const float ref = m[nt][c] - kQdLift;
+        const float ref = m[nt][c] - kQLift;
         w[c] = in0 ? ex2_fast(z[nt][c] - ref) : 0.f;
         w[2 + c] = in1 ? ex2_fast(z[nt][2 + c] - ref) : 0.f;
         l[nt][c] += in0 ? w[c] * vi[0] : 0.f;
@@ -608,10 +602,10 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
                    *v3 = &vc[3].x;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      const uint32_t a01 = byte_perm(v0[w], v1[w], 0x5140);
-      const uint32_t a23 = byte_perm(v2[w], v3[w], 0x5140);
-      const uint32_t b01 = byte_perm(v0[w], v1[w], 0x7362);
-      const uint32_t b23 = byte_perm(v2[w], v3[w], 0x7362);
+      const uint32_t a01 = __byte_perm(v0[w], v1[w], 0x5140);
+      const uint32_t a23 = __byte_perm(v2[w], v3[w], 0x5140);
+      const uint32_t b01 = __byte_perm(v0[w], v1[w], 0x7362);
+      const uint32_t b23 = __byte_perm(v2[w], v3[w], 0x7362);
       const uint32_t fa[4] = {e4m3x2_lo(a01), e4m3x2_hi(a01), e4m3x2_lo(a23),
                               e4m3x2_hi(a23)};
       const uint32_t fb[4] = {e4m3x2_lo(b01), e4m3x2_hi(b01), e4m3x2_lo(b23),
@@ -715,7 +709,7 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
       if (lane == 0)
         a.lse_out[row] = sum == 0.f
                              ? -INFINITY
-                             : (log2f(sum) + (M - kQdLift)) * kQdLn2;
+                             : (log2f(sum) + (M - kQLift)) * kQdLn2;
     }
     if (ucl > 1) cluster_sync();  // no CTA leaves while its slices are read
   }
@@ -849,7 +843,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
       pack_bf2q(acc.x * inv, acc.y * inv), pack_bf2q(acc.z * inv, acc.w * inv));
   if (lane == 0)
     a.lse_out[row] =
-        sum == 0.f ? -INFINITY : (log2f(sum) + (M - kQdLift)) * kQdLn2;
+        sum == 0.f ? -INFINITY : (log2f(sum) + (M - kQLift)) * kQdLn2;
 }
 
 // ---------------------------------------------------------------------------

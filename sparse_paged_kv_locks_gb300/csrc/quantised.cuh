@@ -22,6 +22,13 @@ constexpr int kQExpLo = -32, kQExpHi = 31;    // limits of a scale exponent
 
 static_assert(kQOffVE + kPage == kQRec, "record size");
 
+// attention: scores in base 2; weights are 2^(score + value exponent - m + 8),
+// their reference m trails the maximum by at most 7
+constexpr float kQScale = 0.12751743074602467f;  // log2(e) / sqrt(128)
+constexpr float kQLift = 8.f, kQSlack = 7.f;
+// value scales further apart than 2^8 leave fp16 weights too few bits
+constexpr uint32_t kQSpread = 8;
+
 // Where the 16-byte group c (dims 16c .. 16c + 15) of the row in slot s sits
 // in the row.  Both readings of a record from shared memory are then free of
 // bank conflicts: eight lanes that read key rows 2i, 2i + 1, groups 4j .. 4j
