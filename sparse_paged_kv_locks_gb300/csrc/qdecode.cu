@@ -400,9 +400,10 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
   // The weights of a page below fp16's normal numbers, in bins b = 1 .. 4 of
   // 2^(-14 - 24 b) <= w < 2^(-14 - 24 (b - 1)): a bin's weights times 2^(24 b)
   // have all their bits, its products are added with 2^(-24 b).  What is left
-  // out is 2^-118 of the largest contribution.  (z of places without a token is
-  // -infinity: in no bin.)
-  auto binned_weights = [&](const float (&z)[NT][4], const uint4 (&vc)[4]) {
+  // out is 2^-118 of the largest contribution.  Their z become -infinity, as
+  // of places without a token: nothing is left of them for the page's products.
+  auto binned_weights = [&](float (&z)[NT][4], const float (&vi)[2],
+                            const uint4 (&vc)[4]) {
 #pragma unroll 1
     for (int b = 1; b <= kQdBins; ++b) {
       const float up = kQdBin * (float)b;
@@ -417,6 +418,8 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
           const bool here = y >= kQdNormal && y < kQdNormal + kQdBin;
           w[i] = here ? ex2_fast(y) : 0.f;
           some |= here;
+          if (here)
+            l[nt][i & 1] += ex2_fast(y - up) * vi[i >> 1];
         }
         pb0[nt] = movmatrix_trans(pack_h2(w[0], w[1]));
         pb1[nt] = movmatrix_trans(pack_h2(w[2], w[3]));
@@ -448,6 +451,12 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
         }
       }
     }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (z[nt][i] - (m[nt][i & 1] - kQLift) < kQdNormal)
+          z[nt][i] = -INFINITY;
   };
 
   uint32_t phase = 0;
@@ -530,7 +539,7 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
     float z[NT][4];
     const bool far0 = in0 && e2[0] + kQSpread < e_top;
     const bool far1 = in1 && e2[1] + kQSpread < e_top;
-    bool raise = far0 || far1, binned = false;
+    bool raise = far0 || far1;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -574,8 +583,7 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
           low |= in0 && e2[0] + kQSpread < e_top && z[nt][c] < least;
           low |= in1 && e2[1] + kQSpread < e_top && z[nt][2 + c] < least;
         }
-      binned = __any_sync(0xffffffffu, low);
-      if (binned) binned_weights(z, vc);
+      if (__any_sync(0xffffffffu, low)) binned_weights(z, vi, vc);
     }
     uint32_t pb0[NT], pb1[NT];
 #pragma unroll
@@ -588,10 +596,6 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
         w[2 + c] = in1 ? ex2_fast(z[nt][2 + c] - ref) : 0.f;
         l[nt][c] += in0 ? w[c] * vi[0] : 0.f;
         l[nt][c] += in1 ? w[2 + c] * vi[1] : 0.f;
-        if (binned) {  // those below are in already
-          w[c] = z[nt][c] - ref < kQdNormal ? 0.f : w[c];
-          w[2 + c] = z[nt][2 + c] - ref < kQdNormal ? 0.f : w[2 + c];
-        }
       }
       pb0[nt] = movmatrix_trans(pack_h2(w[0], w[1]));
       pb1[nt] = movmatrix_trans(pack_h2(w[2], w[3]));
