@@ -10,13 +10,14 @@
 //
 // Keys take part as they are stored: the e4m3 rows are copied to shared
 // memory, and the query row is the sum of two rows of codes, hi in e4m3 and lo
-// in e5m2, after a power-of-two scale that puts its largest magnitude in (224,
-// 448].  A bf16 number has 8 significant bits.  hi, of 4, leaves a rest of at
-// most 8 of its last places, which lo's 3 bits hold (a rest of 9 to 15 would
-// take 4), so that hi + lo is exact from 2^-6 on, 2^-13 of the row's largest
-// element.  Below, hi's step is 2^-9 and lo, whose own goes down to 2^-16, is
-// off by at most 2^-14, 2^-21 of the row's largest element: what fp32 products
-// with that element lose.  (Both in e4m3, it was 2^-17.)
+// in e5m2, after a power-of-two scale that puts its largest magnitude in [2^11,
+// 2^12).  A bf16 number has 8 significant bits, hi 4, lo 3.  Up to 448 hi is the
+// nearest code and lo takes the rest, at most 8 of the last places (9 to 15
+// would need 4 bits); beyond, lo is the nearest code and hi takes the rest, at
+// most 16 places and 256.  So hi + lo is exact from 2^-6 on, 2^-17 of the row's
+// largest element; below, hi's step is 2^-9 and lo, whose own goes down to
+// 2^-16, is off by at most 2^-14, 2^-25 of the row's largest element: less than
+// fp32 products with that element lose.
 //
 // A key's scale multiplies its column of scores.  Value codes are widened to
 // fp16, a page's rows scaled by 2^(e - E), E the largest exponent of the
@@ -235,6 +236,11 @@ __device__ __forceinline__ uint32_t e5m2x2_from(float lo, float hi) {
   return r;
 }
 
+// .. and back: an e5m2 code is the high byte of the fp16 number
+__device__ __forceinline__ float2 e5m2x2_to(uint32_t codes) {
+  return __half22float2(u32_as_h2(__byte_perm(codes, 0u, 0x1404)));
+}
+
 // two fp32 numbers in one 64-bit register pair
 __device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
   uint64_t r;
@@ -429,11 +435,13 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
       for (int k = 0; k < 4; ++k)
         top = fmaxf(top, fmaxf(fabsf(bf16_lo(x[k])), fabsf(bf16_hi(x[k]))));
     }
-    // least e with top <= 448 * 2^e
-    const uint32_t tb = __float_as_uint(top);
-    const int e =
-        max(-100, (int)(tb >> 23) - 135 + ((tb & 0x7fffffu) > 0x600000u));
+    // largest magnitude to [2^11, 2^12)
+    const int e = max(-100, (int)(__float_as_uint(top) >> 23) - 127 - 11);
     const float down = exp2_int(-e);
+    // what e5m2 has to take of a number beyond e4m3's largest
+    auto beyond = [](float a, float code) -> float {
+      return fabsf(a) > 448.f ? code : 0.f;
+    };
     // codes have no infinity: a row that holds one has scores that are not
     // numbers
     const float f = isinf(top) ? top - top : exp2_int(e) * kQScale;
@@ -451,8 +459,11 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
           const float a1 = bf16_hi(x[2 * n2]) * down;
           const float a2 = bf16_lo(x[2 * n2 + 1]) * down;
           const float a3 = bf16_hi(x[2 * n2 + 1]) * down;
+          const float2 b0 = e5m2x2_to(e5m2x2_from(a0, a1));
+          const float2 b1 = e5m2x2_to(e5m2x2_from(a2, a3));
           const uint32_t c =
-              e4m3x2_from(a0, a1) | e4m3x2_from(a2, a3) << 16;
+              e4m3x2_from(a0 - beyond(a0, b0.x), a1 - beyond(a1, b0.y)) |
+              e4m3x2_from(a2 - beyond(a2, b1.x), a3 - beyond(a3, b1.y)) << 16;
           const float2 h0 = __half22float2(u32_as_h2(e4m3x2_lo(c)));
           const float2 h1 = __half22float2(u32_as_h2(e4m3x2_hi(c)));
           hi[2 * k + n2] = c;

@@ -422,8 +422,8 @@ def test_shared_values_of_the_whole_scale_range(batch, G, h_kv, np_):
 # ---------------------------------------------------------------------------
 def shared_query_error(q):
     """hi + lo of the shared pages' query: scaled by a power of two that puts
-    the row's largest in (224, 448], off by 2^-14 at most below 2^-6."""
-    unit = 2.0 ** np.ceil(np.log2(np.abs(q).max(1, keepdims=True) / 448))
+    the row's largest in [2^11, 2^12), off by 2^-14 at most below 2^-6."""
+    unit = 2.0 ** (np.floor(np.log2(np.abs(q).max(1, keepdims=True))) - 11)
     return np.where(np.abs(q) < 2.0 ** -6 * unit, 2.0 ** -14 * unit, 0.0)
 
 
