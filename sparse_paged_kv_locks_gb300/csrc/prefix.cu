@@ -43,7 +43,7 @@
 // scores, in which the tensor core is busy with both row tiles for about 2,650
 // of 4,300.  The product of keys and query reads shared memory at 122 bytes a
 // cycle of 128 and runs at 70% of its rate.  A 128K prefix for 64 sequences and
-// 64 query heads takes 276 us in this form (300 with one row tile to a CTA);
+// 64 query heads takes 277 us in this form (300 with one row tile to a CTA);
 // with half of that product left out 24 us less, of the other 18, without the
 // exponentials 18, without the loads of key scales 19; without the stores of
 // widened values or of mended keys the same.  For few rows, the start and end
@@ -89,8 +89,8 @@ constexpr long long kPfMinShared = 12288;
 // A tile with value rows more than 2^kQSpread below the largest scale so far
 // takes its weights and values in bf16 (far_tile).  Twice the time, for tiles
 // after an outlier's alone: with an infinity in its first page a 128K prefix for
-// 64 sequences takes 620 us instead of 276 (the range that holds it is the last
-// to end), one of 32K for 32 49 us instead of 47.
+// 64 sequences takes 616 us instead of 277 (the range that holds it is the last
+// to end), one of 32K for 32 49 us instead of 48.
 
 // ---------------------------------------------------------------------------
 // tcgen05
@@ -614,7 +614,8 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
           m = to;
           l *= fall;
           tm_wait_st();
-          for (int k = 0; k < 2 * c; ++k) {  // this tile's weights so far
+          // this tile's weights so far, rounded a second time
+          for (int k = 0; k < 2 * c; ++k) {
             uint32_t w[16];
             tm_ld16(w, mine + 16 * k);
             tm_wait_ld();

@@ -56,8 +56,8 @@ constexpr float kQdLn2 = 0.69314718055994531f;
 // Weights below fp16's normal numbers, of rows whose value scale is more than
 // 2^kQSpread below the largest of the pages that raised m, are taken in bins of
 // 24 powers of two each.  Ordinary pages pay two comparisons; with an infinity in
-// every sequence's first page, 256 lists of 128 pages take 43 us instead of 30
-// and a dense ragged batch 80 instead of 70.
+// every sequence's first page, 256 lists of 128 pages take 42 us instead of 29
+// and a dense ragged batch 81 instead of 70.
 constexpr float kQdNormal = -14.f, kQdBin = 24.f;
 constexpr int kQdBins = 4;
 

@@ -5,10 +5,11 @@
 // a row, 16 numbers each, so the maximum needs three shuffles and a lane's 16
 // codes are one aligned group of the record; a warp holds four (token, head)
 // rows at a time.  Reads and writes are each done once; both kernels are
-// bound by memory: four prompts of 101K tokens and 8 heads 113 us (5.6 TB/s;
-// 125 us before the rows were loaded ahead of their places), two prompts of
-// 32K read back 66-69 us (5.9-6.1 TB/s); one token per sequence, or a page,
-// 4-6 us, by the launch and three dependent loads.
+// bound by memory: four prompts of 101K tokens and 8 heads 110 us (5.8 TB/s;
+// 125 us before the rows were loaded ahead of their places; from fp32 150 us),
+// two prompts of 32K read back 66 us (6.1 TB/s; as fp32 134 us, 5.0 TB/s); one
+// token per sequence, or a page, 2 us among others and 8-9 us alone on cold data,
+// by the launch and three dependent loads.
 #include "launch.h"
 #include "quantised.cuh"
 
