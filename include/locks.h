@@ -501,8 +501,8 @@ void locks_decoder_destroy(locks_decoder_t *decoder);
  * is at most 2^-4 of it, or 2^(e-10) where that is more.  The division is
  * exact, so every platform finds the same codes.  Infinities, and magnitudes
  * above 448 * 2^31, become +-448 * 2^31; NaN stays NaN and has no part in the
- * maximum; rows below 448 * 2^-32 keep e = -32 and lose low bits.  A number read back,
- * code * 2^e, is exact in bf16 and fp32.
+ * maximum; rows below 448 * 2^-32 keep e = -32 and lose low bits.  A number
+ * read back, code * 2^e, is exact in bf16 and fp32.
  * Records of zeros, as of a new cache, read as rows of zeros, and take part in
  * attention as such where a length covers them.
  * ------------------------------------------------------------------------ */

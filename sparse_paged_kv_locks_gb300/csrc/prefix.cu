@@ -570,88 +570,89 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
       tm_fence_after();
       const uint32_t there = sh.there[par][0] | sh.there[par][1];
       const bool far = sh.far[par];
-      if (far)
+      if (far) {
         far_tile(par, there, j > 0);
-      else
-      // 64 columns at a time: their weights go over the scores they come
-      // from, in columns that have been read
-      for (int c = 0; c < 2; ++c) {
-        uint64_t x[32];
-        {
-          uint32_t s0[32], s1[32];
-          tm_ld32(s0, mine + 64 * c);
-          tm_ld32(s1, mine + 64 * c + 32);
-          tm_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            x[i] = pack2(s0[2 * i], s0[2 * i + 1]);
-            x[16 + i] = pack2(s1[2 * i], s1[2 * i + 1]);
-          }
-        }
-        float top = -INFINITY;
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          const int pg = 4 * c + p;
-          float t4[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float4 k4 =
-                reinterpret_cast<const float4 *>(sh.k_scale[par])[4 * pg + i];
-            uint64_t &x0 = x[8 * p + 2 * i], &x1 = x[8 * p + 2 * i + 1];
-            x0 = mul2(x0, pack2(k4.x, k4.y));
-            x1 = mul2(x1, pack2(k4.z, k4.w));
-            const float2 u = unpack2(x0), v = unpack2(x1);
-            t4[i] = fmaxf(max3(u.x, u.y, v.x), v.y);
-          }
-          const float t1 = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]);
-          if (there >> pg & 1)
-            top = fmaxf(top, fmaf(t1, f, sh.v_exp[par][pg]));
-        }
-        const bool raise = top > m + kQSlack;
-        if (__any_sync(0xffffffffu, raise)) {  // rare after the first tiles
-          const float to = raise ? top : m;
-          const float fall = to == m ? 1.f : ex2_fast(m - to);
-          m = to;
-          l *= fall;
-          tm_wait_st();
-          // this tile's weights so far, rounded a second time
-          for (int k = 0; k < 2 * c; ++k) {
-            uint32_t w[16];
-            tm_ld16(w, mine + 16 * k);
+      } else {
+        // 64 columns at a time: their weights go over the scores they come
+        // from, in columns that have been read
+        for (int c = 0; c < 2; ++c) {
+          uint64_t x[32];
+          {
+            uint32_t s0[32], s1[32];
+            tm_ld32(s0, mine + 64 * c);
+            tm_ld32(s1, mine + 64 * c + 32);
             tm_wait_ld();
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float2 v = __half22float2(u32_as_h2(w[i]));
-              w[i] = h2_as_u32(__floats2half2_rn(v.x * fall, v.y * fall));
+              x[i] = pack2(s0[2 * i], s0[2 * i + 1]);
+              x[16 + i] = pack2(s1[2 * i], s1[2 * i + 1]);
             }
-            tm_st16(mine + 16 * k, w);
           }
-          if (j > 0) rescale(fall);
+          float top = -INFINITY;
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const int pg = 4 * c + p;
+            float t4[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float4 k4 =
+                  reinterpret_cast<const float4 *>(sh.k_scale[par])[4 * pg + i];
+              uint64_t &x0 = x[8 * p + 2 * i], &x1 = x[8 * p + 2 * i + 1];
+              x0 = mul2(x0, pack2(k4.x, k4.y));
+              x1 = mul2(x1, pack2(k4.z, k4.w));
+              const float2 u = unpack2(x0), v = unpack2(x1);
+              t4[i] = fmaxf(max3(u.x, u.y, v.x), v.y);
+            }
+            const float t1 = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]);
+            if (there >> pg & 1)
+              top = fmaxf(top, fmaf(t1, f, sh.v_exp[par][pg]));
+          }
+          const bool raise = top > m + kQSlack;
+          if (__any_sync(0xffffffffu, raise)) {  // rare after the first tiles
+            const float to = raise ? top : m;
+            const float fall = to == m ? 1.f : ex2_fast(m - to);
+            m = to;
+            l *= fall;
+            tm_wait_st();
+            // this tile's weights so far, rounded a second time
+            for (int k = 0; k < 2 * c; ++k) {
+              uint32_t w[16];
+              tm_ld16(w, mine + 16 * k);
+              tm_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float2 v = __half22float2(u32_as_h2(w[i]));
+                w[i] = h2_as_u32(__floats2half2_rn(v.x * fall, v.y * fall));
+              }
+              tm_st16(mine + 16 * k, w);
+            }
+            if (j > 0) rescale(fall);
+          }
+          uint32_t w[32];
+          const uint64_t ff = pack2(f, f);
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const int pg = 4 * c + p;
+            const float add = sh.v_exp[par][pg] - (m - kQLift);
+            const uint64_t aa = pack2(add, add);
+            uint64_t sum[2] = {0, 0};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float2 z = unpack2(fma2(x[8 * p + i], ff, aa));
+              const float u = ex2_fast(z.x), v = ex2_fast(z.y);
+              sum[i & 1] = add2(sum[i & 1], pack2(u, v));
+              w[8 * p + i] = h2_as_u32(__floats2half2_rn(u, v));
+            }
+            if (there >> pg & 1) {
+              const float2 t2 = unpack2(add2(sum[0], sum[1]));
+              l = fmaf(t2.x + t2.y, sh.v_inv[par][pg], l);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) w[8 * p + i] = 0u;
+            }
+          }
+          tm_st32(mine + 32 * c, w);
         }
-        uint32_t w[32];
-        const uint64_t ff = pack2(f, f);
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          const int pg = 4 * c + p;
-          const float add = sh.v_exp[par][pg] - (m - kQLift);
-          const uint64_t aa = pack2(add, add);
-          uint64_t sum[2] = {0, 0};
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float2 z = unpack2(fma2(x[8 * p + i], ff, aa));
-            const float u = ex2_fast(z.x), v = ex2_fast(z.y);
-            sum[i & 1] = add2(sum[i & 1], pack2(u, v));
-            w[8 * p + i] = h2_as_u32(__floats2half2_rn(u, v));
-          }
-          if (there >> pg & 1) {
-            const float2 t2 = unpack2(add2(sum[0], sum[1]));
-            l = fmaf(t2.x + t2.y, sh.v_inv[par][pg], l);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[8 * p + i] = 0u;
-          }
-        }
-        tm_st32(mine + 32 * c, w);
       }
       tm_wait_st();
       tm_fence_before();
