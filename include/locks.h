@@ -558,7 +558,8 @@ locks_status_t locks_dequantise_kv(
  * (idx NULL: every page), outputs, workspace and status bits, with K and V
  * the numbers that the records stand for.  q and o_out must be 16-byte
  * aligned.  The query takes part in fp16 after a power-of-two scale per
- * head, sums and softmax statistics in fp32.  Weights have 11 bits, whatever
+ * head, scores, sums and softmax statistics in fp32 (tokens of equal scores
+ * have equal weights however large those are).  Weights have 11 bits, whatever
  * the value rows' scales: of rows within 2^8 of the largest scale, weights
  * below 2^-22 of the largest lose bits, which moves an output by at most 2^-25
  * of the largest weight times the sum of |v| in its dim.

@@ -20,10 +20,9 @@
 // fp32 products with that element lose.
 //
 // A key's scale multiplies its column of scores.  Value codes are widened to
-// fp16, a page's rows scaled by 2^(e - E), E the largest exponent of the
-// page, which joins the weights' exponent: exact, since a tile with rows more
-// than 2^8 below the largest scale so far takes another form (far_tile: codes
-// and weights in bf16, the weights as hi + lo).
+// fp16, scaled by 2^(e - E), E the largest exponent so far, in whose unit the
+// sums are: exact, since a tile with rows more than 2^8 below E takes another
+// form (far_tile: codes and weights in bf16, the weights as hi + lo).
 //
 // Rows of a record are swizzled by f(s) = (s & 6) ^ 5 (s & 1), rows of the
 // tensor core's operand by s & 7.  The two agree on even rows; an odd row's
@@ -43,7 +42,7 @@
 // scores, in which the tensor core is busy with both row tiles for about 2,650
 // of 4,300.  The product of keys and query reads shared memory at 122 bytes a
 // cycle of 128 and runs at 70% of its rate.  A 128K prefix for 64 sequences and
-// 64 query heads takes 277 us in this form (300 with one row tile to a CTA);
+// 64 query heads takes 273 us in this form (300 with one row tile to a CTA);
 // with half of that product left out 24 us less, of the other 18, without the
 // exponentials 18, without the loads of key scales 19; without the stores of
 // widened values or of mended keys the same.  For few rows, the start and end
@@ -89,8 +88,8 @@ constexpr long long kPfMinShared = 12288;
 // A tile with value rows more than 2^kQSpread below the largest scale so far
 // takes its weights and values in bf16 (far_tile).  Twice the time, for tiles
 // after an outlier's alone: with an infinity in its first page a 128K prefix for
-// 64 sequences takes 616 us instead of 277 (the range that holds it is the last
-// to end), one of 32K for 32 49 us instead of 48.
+// 64 sequences takes 511 us instead of 273 (the range that holds it is the last
+// to end), one of 32K for 32 48 us either way.
 
 // ---------------------------------------------------------------------------
 // tcgen05
@@ -296,11 +295,10 @@ struct PfArgs {
 
 template <int R>
 struct PfShared {
-  // of tile j, at j & 1: scales of the keys, E and 2^-E of the pages' values,
-  // and which pages are there (a widening warp's each)
+  // of tile j, at j & 1: scales of the keys, the largest value scale so far,
+  // which pages are there (a widening warp's each)
   float k_scale[2][kPfTile];
-  float v_exp[2][kPfPages], v_inv[2][kPfPages];
-  uint32_t there[2][kPfWiden];
+  uint32_t v_top[2], there[2][kPfWiden];
   // whether the tile is a far one, then the scales of its values by token; the
   // widening warps' largest and least of them
   alignas(16) uint8_t v_token[2][kPfTile];
@@ -483,9 +481,14 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
     const uint32_t mine =
         tm + tile * kPfColumns + ((uint32_t)((wid & 3) * 32) << 16);
     float m = -INFINITY, l = 0.f;
+    uint32_t e_top = 0;  // unit of the sums
+    // a zero that the compiler does not know: mul.rn and add.rn of two numbers
+    // at once are made one fma with one rounding, an fma and an add are not
+    const float zero = __int_as_float(*(volatile int *)&sh.dead);
     bool ok = true;
     // rescales the sums in tensor memory
     auto rescale = [&](float fall) {
+      tm_wait_st();
       for (int k = 0; k < 8; ++k) {
         uint32_t o[16];
         tm_ld16(o, mine + kPfColO + 16 * k);
@@ -496,48 +499,41 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
         tm_st16(mine + kPfColO + 16 * k, o);
       }
     };
-    // A far tile: every token's own value scale in its weight (so that the
-    // reference is the largest term's, and no page's rows are rounded beside a
-    // larger one), the weights as hi + lo in bf16, whose range is fp32's: 16
-    // bits at any size.  Hi and lo of a page lie over the 16 columns of its
-    // scores, 8 columns each.
+    // raises the reference to `top` in lanes whose scores pass it by too much
+    auto raise = [&](float top, bool sums) -> float {
+      const float to = top > m + kQSlack ? top : m;
+      const float fall = to == m ? 1.f : ex2_fast(m - to);
+      m = to;
+      l *= fall;
+      if (sums) rescale(fall);
+      return fall;
+    };
+    // A far tile: a token's value scale in its factor, the factors as hi + lo in
+    // bf16, whose range is fp32's: 16 bits at any size.  Hi and lo of a page lie
+    // over the 16 columns of its scores, 8 columns each.
     auto far_tile = [&](int par, uint32_t there, bool sums) {
-      auto score = [&](uint32_t s, int t, uint32_t e) -> float {
-        return fmaf(__uint_as_float(s) * sh.k_scale[par][t], f,
-                    (float)((int)e - 127));
-      };
-      auto scale = [&](const uint4 &e, int i) -> uint32_t {
-        const uint32_t w = i < 4 ? e.x : i < 8 ? e.y : i < 12 ? e.z : e.w;
-        return w >> 8 * (i & 3) & 255u;
-      };
-      const uint4 *scales = reinterpret_cast<const uint4 *>(sh.v_token[par]);
       float top = -INFINITY;
 #pragma unroll 1
       for (int pg = 0; pg < kPfPages; ++pg) {
         uint32_t s[16];
         tm_ld16(s, mine + 16 * pg);
         tm_wait_ld();
-        const uint4 e = scales[pg];
         if (there >> pg & 1) {
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            top = fmaxf(top, score(s[i], kPage * pg + i, scale(e, i)));
+            top = fmaxf(top, __uint_as_float(s[i]) *
+                                 sh.k_scale[par][kPage * pg + i]);
         }
       }
-      const bool raise = top > m + kQSlack;
-      if (__any_sync(0xffffffffu, raise)) {
-        const float to = raise ? top : m;
-        const float fall = to == m ? 1.f : ex2_fast(m - to);
-        m = to;
-        l *= fall;
-        if (sums) rescale(fall);
-      }
+      top *= f;
+      if (__any_sync(0xffffffffu, top > m + kQSlack)) raise(top, sums);
 #pragma unroll 1
       for (int pg = 0; pg < kPfPages; ++pg) {
         uint32_t s[16], w[16];
         tm_ld16(s, mine + 16 * pg);
         tm_wait_ld();
-        const uint4 e = scales[pg];
+        const uint4 e4 = reinterpret_cast<const uint4 *>(sh.v_token[par])[pg];
+        const uint32_t e[4] = {e4.x, e4.y, e4.z, e4.w};
         const bool here = there >> pg & 1;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -545,11 +541,13 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const int t = 2 * i + k;
-            const uint32_t ev = scale(e, t);
-            u[k] = here ? ex2_fast(score(s[t], kPage * pg + t, ev) -
-                                   (m - kQLift))
-                        : 0.f;
-            if (here) l = fmaf(u[k], __uint_as_float((254u - ev) << 23), l);
+            const uint32_t ev = e[t >> 2] >> 8 * (t & 3) & 255u;
+            const float x = __uint_as_float(s[t]) *
+                            sh.k_scale[par][kPage * pg + t];
+            const float v =
+                here ? ex2_fast(__fmul_rn(x, f) - (m - kQLift)) : 0.f;
+            l += v;
+            u[k] = here ? v * exp2_int((int)ev - (int)e_top) : 0.f;
           }
           const __nv_bfloat162 hi = __floats2bfloat162_rn(u[0], u[1]);
           const __nv_bfloat162 lo = __floats2bfloat162_rn(
@@ -570,6 +568,11 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
       tm_fence_after();
       const uint32_t there = sh.there[par][0] | sh.there[par][1];
       const bool far = sh.far[par];
+      if (sh.v_top[par] != e_top) {  // larger values than before
+        if (j > 0)
+          rescale(exp2_int(max(-126, (int)e_top - (int)sh.v_top[par])));
+        e_top = sh.v_top[par];
+      }
       if (far) {
         far_tile(par, there, j > 0);
       } else {
@@ -604,15 +607,12 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
               t4[i] = fmaxf(max3(u.x, u.y, v.x), v.y);
             }
             const float t1 = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]);
-            if (there >> pg & 1)
-              top = fmaxf(top, fmaf(t1, f, sh.v_exp[par][pg]));
+            if (there >> pg & 1) top = fmaxf(top, t1);
           }
-          const bool raise = top > m + kQSlack;
-          if (__any_sync(0xffffffffu, raise)) {  // rare after the first tiles
-            const float to = raise ? top : m;
-            const float fall = to == m ? 1.f : ex2_fast(m - to);
-            m = to;
-            l *= fall;
+          top *= f;
+          if (__any_sync(0xffffffffu, top > m + kQSlack)) {
+            // rare after the first tiles
+            const float fall = raise(top, j > 0);
             tm_wait_st();
             // this tile's weights so far, rounded a second time
             for (int k = 0; k < 2 * c; ++k) {
@@ -626,26 +626,29 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
               }
               tm_st16(mine + 16 * k, w);
             }
-            if (j > 0) rescale(fall);
           }
           uint32_t w[32];
           const uint64_t ff = pack2(f, f);
+          // scores rounded before the reference is taken off, as it was: equal
+          // ones stay equal and the largest differs from it by nothing, where a
+          // difference rounded alone holds the reference's own rounding (at
+          // 10^11 up to 4096; 3 us of 273)
+          const float ref = kQLift - m;
+          const uint64_t aa = pack2(ref, ref), zz = pack2(zero, zero);
 #pragma unroll
           for (int p = 0; p < 4; ++p) {
             const int pg = 4 * c + p;
-            const float add = sh.v_exp[par][pg] - (m - kQLift);
-            const uint64_t aa = pack2(add, add);
             uint64_t sum[2] = {0, 0};
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const float2 z = unpack2(fma2(x[8 * p + i], ff, aa));
+              const float2 z = unpack2(add2(fma2(x[8 * p + i], ff, zz), aa));
               const float u = ex2_fast(z.x), v = ex2_fast(z.y);
               sum[i & 1] = add2(sum[i & 1], pack2(u, v));
               w[8 * p + i] = h2_as_u32(__floats2half2_rn(u, v));
             }
             if (there >> pg & 1) {
               const float2 t2 = unpack2(add2(sum[0], sum[1]));
-              l = fmaf(t2.x + t2.y, sh.v_inv[par][pg], l);
+              l += t2.x + t2.y;
             } else {
 #pragma unroll
               for (int i = 0; i < 8; ++i) w[8 * p + i] = 0u;
@@ -669,6 +672,7 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
       return (size_t)split * rows * a.h_kv +
              (size_t)(r / a.G) * a.h_kv * a.G + (size_t)h * a.G + r % a.G;
     };
+    const float unit = exp2_int((int)e_top - 127);
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int r0 = row - lane + 16 * half + (lane >> 2);
@@ -682,11 +686,13 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (r0 < rows && ok)
-            *reinterpret_cast<float2 *>(d0 + 32 * c + 8 * i) = make_float2(
-                __uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]));
+            *reinterpret_cast<float2 *>(d0 + 32 * c + 8 * i) =
+                make_float2(__uint_as_float(o[4 * i]) * unit,
+                            __uint_as_float(o[4 * i + 1]) * unit);
           if (r0 + 8 < rows && ok)
-            *reinterpret_cast<float2 *>(d1 + 32 * c + 8 * i) = make_float2(
-                __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+            *reinterpret_cast<float2 *>(d1 + 32 * c + 8 * i) =
+                make_float2(__uint_as_float(o[4 * i + 2]) * unit,
+                            __uint_as_float(o[4 * i + 3]) * unit);
         }
       }
     }
@@ -928,23 +934,17 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
         uint32_t factor[kPfOwn / 2];
 #pragma unroll
         for (int i = 0; i < kPfOwn / 2; ++i) {
-          const int pg = first + 2 * i + (lane >> 4);
-          uint32_t top = ve[i];
-#pragma unroll
-          for (int o = 1; o < 16; o <<= 1)
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-          if ((lane & 15) == 0) {
-            sh.v_exp[j & 1][pg] = (float)((int)top - 127);
-            sh.v_inv[j & 1][pg] = exp2_int(127 - (int)top);
-          }
-          sh.k_scale[j & 1][kPage * pg + (lane & 15)] =
-              __uint_as_float(ke[i] << 23);
-          if (far) sh.v_token[j & 1][kPage * pg + (lane & 15)] = (uint8_t)ve[i];
-          factor[i] = h2_as_u32(
-              __float2half2_rn(exp2_int(max(-126, (int)ve[i] - (int)top))));
+          const int at = kPage * (first + 2 * i + (lane >> 4)) + (lane & 15);
+          sh.k_scale[j & 1][at] = __uint_as_float(ke[i] << 23);
+          if (far) sh.v_token[j & 1][at] = (uint8_t)ve[i];
+          factor[i] = h2_as_u32(__float2half2_rn(
+              exp2_int(max(-126, min(0, (int)ve[i] - (int)top_e)))));
         }
         if (lane == 0) sh.there[j & 1][own] = now << first;
-        if (lane == 0 && own == 0) sh.far[j & 1] = far;
+        if (lane == 0 && own == 0) {
+          sh.far[j & 1] = far;
+          sh.v_top[j & 1] = top_e;
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(sh.info + (j & 1));
         // O(j - 1) done: its values may go

@@ -2,21 +2,21 @@
 // every query head, x_t = q . k_t / sqrt(128), o = sum softmax(x)_t v_t and
 // lse = ln sum exp(x_t), over the tokens of the listed pages (or of all).
 //
-// With keys k = 2^ek * c, values v = 2^ev * d (codes c, d) and f = log2(e) /
-// sqrt(128),
-//   w_t = 2^(f 2^ek_t (q . c_t) + ev_t - m + 8)
-//   o   = sum w_t d_t / sum w_t 2^-ev_t
-//   lse = ln 2 * (log2(sum w_t 2^-ev_t) + m - 8)
-// so a value's scale is part of its weight and one running reference m (of
-// score plus value exponent) serves both sums.  m is raised, and the sums
-// rescaled, only when a term passes it by more than 2^7: weights stay below
-// 2^15 and, in fp16, keep full precision down to 2^-22 of the largest
-// contribution and some down to 2^-32.  A row whose value scale lies far below
-// the one that m follows gets its weight in a bin of its own (kQdBins), with
-// full precision down to 2^-118: the larger row may be zero in the dims that
-// this one fills.  Codes are exact in fp16, and so is
-// the query after a power-of-two scale per head (elements 2^-22 below its
-// largest lose bits); products, sums and references are fp32.
+// With keys k = 2^ek * c, values v = 2^ev * d (codes c, d), f = log2(e) /
+// sqrt(128) and E the largest ev so far,
+//   w_t = 2^(f 2^ek_t (q . c_t) - m + 8)
+//   o   = 2^E sum w_t 2^(ev_t - E) d_t / sum w_t
+//   lse = ln 2 * (log2(sum w_t) + m - 8)
+// so a value's scale is part of its factor in the product.  The reference m
+// follows scores alone and is taken off scores rounded like itself, which leaves
+// equal scores equal however large they are.  m is raised, and
+// the sums rescaled, only when a score passes it by more than 2^7: factors stay
+// below 2^15 and, in fp16, keep full precision down to 2^-22 of the largest
+// weight and some down to 2^-32.  A row whose scale lies far below E gets its
+// factor in a bin of its own (kQdBins), with full precision down to 2^-118: the
+// larger rows may be zero in the dims that this one fills.  Codes are exact in
+// fp16, and so is the query after a power-of-two scale per head (elements 2^-22
+// below its largest lose bits); products, sums and references are fp32.
 //
 // Bound: memory, 4128 bytes per listed page and KV head.  One bulk copy
 // brings a record into a warp's private ring in shared memory, so the warps
@@ -53,11 +53,11 @@ constexpr int kQdMinRun = 12, kQdMinRunBeside = 2;
 // per CTA (a short sequence leaves its CTA idle, a long one would keep it)
 constexpr int kQdUnitPages = 64;
 constexpr float kQdLn2 = 0.69314718055994531f;
-// Weights below fp16's normal numbers, of rows whose value scale is more than
-// 2^kQSpread below the largest of the pages that raised m, are taken in bins of
-// 24 powers of two each.  Ordinary pages pay two comparisons; with an infinity in
-// every sequence's first page, 256 lists of 128 pages take 42 us instead of 29
-// and a dense ragged batch 81 instead of 70.
+// Factors below fp16's normal numbers, of rows whose value scale is more than
+// 2^kQSpread below the largest so far, are taken in bins of 24 powers of two
+// each.  Ordinary pages pay two comparisons; with an infinity in every
+// sequence's first page, 256 lists of 128 pages take 44 us instead of 29 and a
+// dense ragged batch 81 instead of 69.
 constexpr float kQdNormal = -14.f, kQdBin = 24.f;
 constexpr int kQdBins = 4;
 
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
   // sums: tile i holds dims 16 g + 2 i (elements 0, 1) and 16 g + 2 i + 1
   // (2, 3) of heads 8 nt + 2t (0, 2) and 8 nt + 2t + 1 (1, 3)
   float o[NT][8][4], m[NT][2], l[NT][2];
-  uint32_t e_top = 0;  // largest value scale of the pages that raised m
+  uint32_t e_top = 0;  // largest value scale so far: the sums' unit, E + 127
   auto reset = [&]() {
     e_top = 0;
 #pragma unroll
@@ -333,6 +333,7 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
       const int2 sp = lists.span(u);
       whole = !a.beside && sp.x >= pb && sp.y <= pe;
     }
+    const float unit = exp2_int((int)e_top - 127);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -345,7 +346,7 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
         if (hd >= a.G) continue;
         if (whole) {
           const size_t row = (size_t)b * h_q + (size_t)h * a.G + hd;
-          const float inv = ls == 0.f ? 0.f : 1.f / ls;
+          const float inv = ls == 0.f ? 0.f : unit / ls;
           uint4 *dst = reinterpret_cast<uint4 *>(a.o_out + row * kDim + 16 * g);
           uint32_t w[8];
 #pragma unroll
@@ -366,8 +367,9 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
           float4 *dst = reinterpret_cast<float4 *>(po + 16 * g);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            dst[i] = make_float4(o[nt][2 * i][c], o[nt][2 * i][2 + c],
-                                 o[nt][2 * i + 1][c], o[nt][2 * i + 1][2 + c]);
+            dst[i] = make_float4(
+                o[nt][2 * i][c] * unit, o[nt][2 * i][2 + c] * unit,
+                o[nt][2 * i + 1][c] * unit, o[nt][2 * i + 1][2 + c] * unit);
           if (g == 0) *ml = make_float2(m[nt][c], ls);
         }
       }
@@ -397,16 +399,17 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
       ring_s + kQOffV + (2 * t + 1) * kDim + 16 * q_group(g, 2 * t + 1);
   const uint32_t e_at = ring_s + kQOffKE + g;
 
-  // The weights of a page below fp16's normal numbers, in bins b = 1 .. 4 of
-  // 2^(-14 - 24 b) <= w < 2^(-14 - 24 (b - 1)): a bin's weights times 2^(24 b)
+  // The factors of a page below fp16's normal numbers, in bins b = 1 .. 4 of
+  // 2^(-14 - 24 b) <= w < 2^(-14 - 24 (b - 1)): a bin's factors times 2^(24 b)
   // have all their bits, its products are added with 2^(-24 b).  What is left
-  // out is 2^-118 of the largest contribution.  Their z become -infinity, as
+  // out is 2^-118 of the largest contribution.  Their y become -infinity, as
   // of places without a token: nothing is left of them for the page's products.
-  auto binned_weights = [&](float (&z)[NT][4], const float (&vi)[2],
+  auto binned_weights = [&](float (&y)[NT][4], const uint32_t (&e2)[2],
                             const uint4 (&vc)[4]) {
+    const float unit[2] = {(float)((int)e2[0] - (int)e_top),
+                           (float)((int)e2[1] - (int)e_top)};
 #pragma unroll 1
     for (int b = 1; b <= kQdBins; ++b) {
-      const float up = kQdBin * (float)b;
       uint32_t pb0[NT], pb1[NT];
       bool some = false;
 #pragma unroll
@@ -414,12 +417,10 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
         float w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float y = z[nt][i] - (m[nt][i & 1] - kQLift) + up;
-          const bool here = y >= kQdNormal && y < kQdNormal + kQdBin;
-          w[i] = here ? ex2_fast(y) : 0.f;
+          const float at = y[nt][i] + unit[i >> 1] + kQdBin * (float)b;
+          const bool here = at >= kQdNormal && at < kQdNormal + kQdBin;
+          w[i] = here ? ex2_fast(at) : 0.f;
           some |= here;
-          if (here)
-            l[nt][i & 1] += ex2_fast(y - up) * vi[i >> 1];
         }
         pb0[nt] = movmatrix_trans(pack_h2(w[0], w[1]));
         pb1[nt] = movmatrix_trans(pack_h2(w[2], w[3]));
@@ -455,8 +456,10 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (z[nt][i] - (m[nt][i & 1] - kQLift) < kQdNormal)
-          z[nt][i] = -INFINITY;
+        if (y[nt][i] + unit[i >> 1] < kQdNormal) {
+          l[nt][i & 1] += ex2_fast(y[nt][i]);
+          y[nt][i] = -INFINITY;
+        }
   };
 
   uint32_t phase = 0;
@@ -494,13 +497,11 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
     vc[1] = lds128(v_at1 + off);
     vc[2] = lds128(v_at + off + 8 * kDim);
     vc[3] = lds128(v_at1 + off + 8 * kDim);
-    float ks[2], ev[2], vi[2];
+    float ks[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       ks[r] = __uint_as_float(ek[r] << 23);
       e2[r] = q_scale_byte(e2[r]);
-      ev[r] = (float)((int)e2[r] - 127);
-      vi[r] = __uint_as_float((254u - e2[r]) << 23);
     }
     if (ntok < kPage) {  // rows past the end hold anything
 #pragma unroll
@@ -535,26 +536,40 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
       for (int i = 0; i < 4; ++i) s[nt][i] += s2[nt][i];
 
     // weights
-    const bool in0 = g < ntok, in1 = g + 8 < ntok;
-    float z[NT][4];
-    const bool far0 = in0 && e2[0] + kQSpread < e_top;
-    const bool far1 = in1 && e2[1] + kQSpread < e_top;
-    bool raise = far0 || far1;
+    const bool in[2] = {g < ntok, g + 8 < ntok};
+    float y[NT][4];  // log2 of a weight
+    // a scale above all before (the sums' unit follows it), or far below them
+    bool rare = (in[0] && e_top - e2[0] > kQSpread) ||
+                (in[1] && e_top - e2[1] > kQSpread);
+    auto score = [&](int nt, int i) -> float {
+      return __fmul_rn(s[nt][i], f[nt][i & 1] * ks[i >> 1]);
+    };
+    auto log_weights = [&]() {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          y[nt][i] = in[i >> 1] ? score(nt, i) - (m[nt][i & 1] - kQLift)
+                                : -INFINITY;
+    };
+    log_weights();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        z[nt][c] = in0 ? fmaf(s[nt][c], f[nt][c] * ks[0], ev[0]) : -INFINITY;
-        z[nt][2 + c] =
-            in1 ? fmaf(s[nt][2 + c], f[nt][c] * ks[1], ev[1]) : -INFINITY;
-        raise |= fmaxf(z[nt][c], z[nt][2 + c]) > m[nt][c] + kQSlack;
-      }
-    if (__any_sync(0xffffffffu, raise)) {
+      for (int c = 0; c < 2; ++c)
+        rare |= fmaxf(y[nt][c], y[nt][2 + c]) > kQLift + kQSlack;
+    if (__any_sync(0xffffffffu, rare)) {
+      const uint32_t e_was = e_top;
+      e_top = max(e_top, __reduce_max_sync(0xffffffffu,
+                                           max(in[0] ? e2[0] : 0u,
+                                               in[1] ? e2[1] : 0u)));
+      const float unit = exp2_int(max(-126, (int)e_was - (int)e_top));
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float top = fmaxf(z[nt][c], z[nt][2 + c]);
+          float top = fmaxf(in[0] ? score(nt, c) : -INFINITY,
+                            in[1] ? score(nt, 2 + c) : -INFINITY);
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
@@ -564,38 +579,40 @@ __global__ void __launch_bounds__(kQdThreads, NT == 1 ? 3 : 2)
           l[nt][c] *= fall;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            o[nt][i][c] *= fall;
-            o[nt][i][2 + c] *= fall;
+            o[nt][i][c] *= fall * unit;
+            o[nt][i][2 + c] *= fall * unit;
           }
         }
-      // rows far below the scale of those that raised the reference, whose
-      // weight fp16 would round to fewer bits, or to nothing, although the
-      // larger rows may hold zeros in the dims that these do not
-      e_top = max(e_top,
-                  __reduce_max_sync(0xffffffffu, max(in0 ? e2[0] : 0u,
-                                                     in1 ? e2[1] : 0u)));
+      log_weights();
+      // rows far below the largest scale whose weight fp16 would round to fewer
+      // bits, or to nothing, although the larger rows may hold zeros in the
+      // dims that these do not
       bool low = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int r = 0; r < 2; ++r) {
+        const float least = kQdNormal + (float)((int)e_top - (int)e2[r]);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float least = m[nt][c] - kQLift + kQdNormal;
-          low |= in0 && e2[0] + kQSpread < e_top && z[nt][c] < least;
-          low |= in1 && e2[1] + kQSpread < e_top && z[nt][2 + c] < least;
-        }
-      if (__any_sync(0xffffffffu, low)) binned_weights(z, vi, vc);
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            low |= in[r] && e_top - e2[r] > kQSpread &&
+                   y[nt][2 * r + c] < least;
+      }
+      if (__any_sync(0xffffffffu, low)) binned_weights(y, e2, vc);
     }
+    float v_unit[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      v_unit[r] = in[r] ? exp2_int((int)e2[r] - (int)e_top) : 0.f;
     uint32_t pb0[NT], pb1[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float w[4];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const float ref = m[nt][c] - kQLift;
-        w[c] = in0 ? ex2_fast(z[nt][c] - ref) : 0.f;
-        w[2 + c] = in1 ? ex2_fast(z[nt][2 + c] - ref) : 0.f;
-        l[nt][c] += in0 ? w[c] * vi[0] : 0.f;
-        l[nt][c] += in1 ? w[2 + c] * vi[1] : 0.f;
+      for (int i = 0; i < 4; ++i) {
+        w[i] = ex2_fast(y[nt][i]);
+        l[nt][i & 1] += w[i];
+        w[i] *= v_unit[i >> 1];
       }
       pb0[nt] = movmatrix_trans(pack_h2(w[0], w[1]));
       pb1[nt] = movmatrix_trans(pack_h2(w[2], w[3]));

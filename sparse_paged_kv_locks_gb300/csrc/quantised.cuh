@@ -22,8 +22,8 @@ constexpr int kQExpLo = -32, kQExpHi = 31;    // limits of a scale exponent
 
 static_assert(kQOffVE + kPage == kQRec, "record size");
 
-// attention: scores in base 2; weights are 2^(score + value exponent - m + 8),
-// their reference m trails the maximum by at most 7
+// attention: scores in base 2; weights are 2^(score - m + 8), their reference m
+// trails the largest score by at most 7
 constexpr float kQScale = 0.12751743074602467f;  // log2(e) / sqrt(128)
 constexpr float kQLift = 8.f, kQSlack = 7.f;
 // value scales further apart than 2^8 leave fp16 weights too few bits
@@ -51,8 +51,7 @@ __device__ __forceinline__ int q_exponent(float absmax) {
 
 // A value scale's byte as the attention takes it.  Zeroed records, which no row
 // has been written to, hold 0 there: codes of zero, so that any scale stands
-// for the same values, and one of the format's keeps the sums of weights times
-// 2^-e in range.
+// for the same values, and the format's least keeps 2^-127 out of the factors.
 __device__ __forceinline__ uint32_t q_scale_byte(uint32_t b) {
   return max(b, (uint32_t)(kQExpLo + 127));
 }

@@ -613,3 +613,83 @@ def test_queries_of_any_size(scale, form):
         idx = lists(rng, lens, h_kv, k) if k else None
         expect(run_lists(q, rec, tables, lens, idx), qn, rec, tables, lens,
                idx)
+
+
+# ---------------------------------------------------------------------------
+# equal scores
+# ---------------------------------------------------------------------------
+def alike(rng, rec, places, exponent):
+    """The same key, 448 * 2^exponent in dim 3, at all places (page, slot), as
+    an infinity there leaves it; values of scales 2^-6 to 2^6 around 2^-9."""
+    for pg, s in places:
+        r = rec[pg]
+        r[:, Q._PLACE[s]] = 0
+        r[:, Q._PLACE[s, 3]] = 0x7E
+        r[:, 4096 + s] = 127 + exponent
+        r[:, 4112 + s] = 127 - 9 + rng.integers(-6, 7, rec.shape[1])
+
+
+def expect_mean(got, qn, rec, places, exponent):
+    """places [batch][n]: the tokens that share a row's weight equally."""
+    o, lse = (t.double().cpu().numpy() for t in got)
+    batch, h_q, _ = qn.shape
+    h_kv = rec.shape[1]
+    G = h_q // h_kv
+    for b in range(batch):
+        pages, slots = zip(*places[b])
+        for h in range(h_kv):
+            V = Q.read(rec[list(pages), h])[1][range(len(pages)), list(slots)]
+            mean, mass = V.mean(0), np.abs(V).mean(0)
+            tol = 2.0 ** -8 * np.abs(mean) + (2.0 ** -11 + 2.0 ** -13) * mass
+            sl = slice(h * G, (h + 1) * G)
+            bad = np.argwhere(~(np.abs(o[b, sl] - mean) <= tol))
+            assert len(bad) == 0, (b, h, len(bad), bad[:4])
+            x = qn[b, sl, 3] * 448 * 2.0 ** exponent / math.sqrt(128)
+            want = x + math.log(len(pages))
+            assert (np.abs(lse[b, sl] - want) <= 2.0 ** -21 * x).all()
+
+
+# scores of some 80, 2e4, 2e6, 1e11
+LEVELS = [1, 9, 16, 31]
+
+
+@pytest.mark.parametrize("lens,h_kv,room,k", FORMS)
+@pytest.mark.parametrize("G", [4, 12])
+@pytest.mark.parametrize("exponent", LEVELS)
+def test_equal_scores_of_any_size(lens, h_kv, room, k, G, exponent):
+    rng = np.random.default_rng(exponent)
+    rec, tables, _ = layout(rng, lens, h_kv, -9, room)
+    rec[..., 4096:4112] = np.minimum(rec[..., 4096:4112], 127 - 9)
+    q = normal(rng, len(lens), G * h_kv, 128)
+    q[:, :, 3] = 1 + (q[:, :, 3].abs() * 4).round().clamp(max=4) / 4
+    places = []
+    for b, n in enumerate(lens):
+        at = [0, 3, n // 3, n // 2, n - 2, n - 1]   # pages that lists hold
+        if k:
+            at = [0, 3, 9, n - 1]
+        places.append(sorted({(int(tables[b, t // 16]), t % 16) for t in at}))
+        alike(rng, rec, places[-1], exponent)
+    idx = lists(rng, lens, h_kv, k) if k else None
+    expect_mean(run_lists(q, rec, tables, lens, idx), q.double().numpy(), rec,
+                places, exponent)
+
+
+@pytest.mark.parametrize("batch,G,h_kv,np_", SHARED)
+@pytest.mark.parametrize("exponent", LEVELS)
+def test_shared_equal_scores_of_any_size(batch, G, h_kv, np_, exponent):
+    # in one tile, in one range, in several, and in the sequences' own pages
+    rng = np.random.default_rng(exponent)
+    lens = [16 * np_ + int(n) for n in rng.integers(5, 40, batch)]
+    rec, tables, prefix = layout(rng, lens, h_kv, -9, np_=np_)
+    q = normal(rng, batch, G * h_kv, 128)
+    q[:, :, 3] = 1 + (q[:, :, 3].abs() * 4).round().clamp(max=4) / 4
+    shared = [(int(prefix[t // 16]), t % 16)
+              for t in (1, 14, 60, 100, 900, 8 * np_, 16 * np_ - 1)]
+    alike(rng, rec, shared, exponent)
+    places = []
+    for b in range(batch):
+        own = [(int(tables[b, np_]), b % 5)] if b % 2 else []
+        alike(rng, rec, own, exponent)
+        places.append(shared + own)
+    expect_mean(run_shared(q, rec, tables, lens, prefix), q.double().numpy(),
+                rec, places, exponent)
