@@ -1031,14 +1031,14 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
 // 0 ranges: too little to share, every sequence reads the pages itself.
 // (Sequences, KV heads, pages, G = 4 unless given: read by each against once,
 // us, replayed back to back.)
-//   triples below the limit: 8, 8, 128: 12.4 and 13.6; 2, 8, 256: 10.9 and 13.7;
-//     32, 8, 32: 11.4 and 16.1; 64, 8, 16, G = 8: 15.6 and 18.3; 16, 8, 64,
-//     G = 16: 14.0 and 21.7; 128, 1, 64, G = 8: 12.9 and 16.9; but 256, 8, 4,
-//     G = 1: 23.3 and 18.0
-//   above: 8, 8, 256: 21.1 and 15.0; 2, 8, 1024: 21.0 and 20.4; 2, 8, 2048: 29.2
-//     and 27.8; 32, 8, 64: 23.0 and 16.6; 64, 8, 32, G = 8: 19.9 and 20.2; 64,
-//     8, 64, G = 8: 31.4 and 21.0; 16, 8, 128, G = 16: 28.3 and 22.7; 256, 8, 8,
-//     G = 1: 26.9 and 17.8; 128, 1, 128, G = 8: 24.2 and 18.0
+//   triples below the limit: 8, 8, 128: 12.2 and 14.6; 2, 8, 256: 10.8 and
+//     15.0; 32, 8, 32: 11.2 and 17.4; 64, 8, 16, G = 8: 15.6 and 18.5; 16, 8,
+//     64, G = 16: 13.9 and 21.8; 128, 1, 64, G = 8: 12.6 and 17.9; but 256, 8,
+//     4, G = 1: 23.5 and 18.5
+//   above: 8, 8, 256: 20.2 and 16.1; 2, 8, 1024: 20.2 and 21.8; 2, 8, 2048:
+//     27.7 and 29.1; 32, 8, 64: 22.1 and 17.8; 64, 8, 32, G = 8: 20.3 and 20.5;
+//     64, 8, 64, G = 8: 30.1 and 22.3; 16, 8, 128, G = 16: 26.6 and 22.0; 256, 8,
+//     8, G = 1: 27.1 and 18.6; 128, 1, 128, G = 8: 23.3 and 19.1
 // One sequence shares nothing (1, 8, 8192: 64 and 77).  The numbers of SMs and
 // of CTAs that fit on them are this GPU's, written out.
 PrefixPlan prefix_plan(int batch, int h_kv, int G, int pages) {

@@ -20,7 +20,7 @@
 //
 // Bound: memory, 4128 bytes per listed page and KV head.  One bulk copy
 // brings a record into a warp's private ring in shared memory, so the warps
-// run free of one another.  256 lists of 128 pages (135 MB): 29-31 us, 4.3-4.6
+// run free of one another.  256 lists of 128 pages (135 MB): 29-30 us, 4.5-4.7
 // TB/s; copies of the same records in the same numbers that nothing uses take
 // 24.5 us, this kernel without its arithmetic 29 us: what is left is the
 // look-ups before the first copy and the merge after the last.  Two units of
@@ -57,7 +57,7 @@ constexpr float kQdLn2 = 0.69314718055994531f;
 // 2^kQSpread below the largest so far, are taken in bins of 24 powers of two
 // each.  Ordinary pages pay two comparisons; with an infinity in every
 // sequence's first page, 256 lists of 128 pages take 44 us instead of 29 and a
-// dense ragged batch 81 instead of 69.
+// dense ragged batch 82 instead of 70.
 constexpr float kQdNormal = -14.f, kQdBin = 24.f;
 constexpr int kQdBins = 4;
 
