@@ -587,8 +587,9 @@ locks_status_t locks_quantised_decode(
  *                 device status word, as for the other calls
  * Other arguments and errors as locks_quantised_decode, and so the weights; the
  * query of the shared pages takes part as the sum of two 8-bit numbers, exact
- * but for elements below 2^-17 of their head's largest, which are off by at
- * most 2^-25 of that. */
+ * but for elements below 2^-13 of their head's largest, which are off by at
+ * most 2^-21 of that (2^-17 and 2^-25 where the largest is 64 times the mean
+ * or more). */
 locks_status_t locks_prefix_decode(
     const void *q, const void *records, int64_t num_phys_pages,
     const int32_t *prefix_table, int prefix_pages, const int32_t *page_table,

@@ -10,14 +10,15 @@
 //
 // Keys take part as they are stored: the e4m3 rows are copied to shared
 // memory, and the query row is the sum of two rows of codes, hi in e4m3 and lo
-// in e5m2, after a power-of-two scale that puts its largest magnitude in [2^11,
-// 2^12).  A bf16 number has 8 significant bits, hi 4, lo 3.  Up to 448 hi is the
-// nearest code and lo takes the rest, at most 8 of the last places (9 to 15
-// would need 4 bits); beyond, lo is the nearest code and hi takes the rest, at
-// most 16 places and 256.  So hi + lo is exact from 2^-6 on, 2^-17 of the row's
-// largest element; below, hi's step is 2^-9 and lo, whose own goes down to
-// 2^-16, is off by at most 2^-14, 2^-25 of the row's largest element: less than
-// fp32 products with that element lose.
+// in e5m2, after a power-of-two scale that puts its largest magnitude in (224,
+// 448].  A bf16 number has 8 significant bits, hi 4, lo 3: hi is the nearest
+// code, lo the rest, at most 8 of the last places (9 to 15 would need 4 bits).
+// So hi + lo is exact from 2^-6 on, 2^-13 of the row's largest element; below,
+// hi's step is 2^-9 and lo, whose own goes down to 2^-16, is off by at most
+// 2^-14, 2^-21 of the row's largest element.  A row with an outlier, 64 times its
+// mean and more, whose other elements would be there, is scaled to [2^11,
+// 2^12): beyond 448 lo is the nearest code and hi the rest, at most 16 places and 256,
+// and the others lose 2^-25 of the largest, less than fp32 products with it do.
 //
 // A key's scale multiplies its column of scores.  Value codes are widened to
 // fp16, scaled by 2^(e - E), E the largest exponent so far, in whose unit the
@@ -424,56 +425,82 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
         a.q + ((size_t)(row / a.G) * a.h_kv * a.G + (size_t)h * a.G +
                row % a.G) * kDim);
     const bool in = row < rows;
-    float top = 0.f;
-#pragma unroll
+    // The largest magnitude and, roughly, the sum of all.  (Loops of the start
+    // and of rare paths are kept short: unrolled, their instructions come from
+    // far, 1 us of 15 for 8 sequences and 256 pages.)
+    const __nv_bfloat162 none = __floats2bfloat162_rn(0.f, 0.f);
+    __nv_bfloat162 most[2] = {none, none}, sums[4] = {none, none, none, none};
+#pragma unroll 8
     for (int i = 0; i < 16; ++i) {
       const uint4 v = in ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
       const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        top = fmaxf(top, fmaxf(fabsf(bf16_lo(x[k])), fabsf(bf16_hi(x[k]))));
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t size = x[k] & 0x7fff7fffu;
+        const __nv_bfloat162 a =
+            *reinterpret_cast<const __nv_bfloat162 *>(&size);
+        most[k & 1] = __hmax2(most[k & 1], a);
+        sums[k] = __hadd2(sums[k], a);
+      }
     }
-    // largest magnitude to [2^11, 2^12)
-    const int e = max(-100, (int)(__float_as_uint(top) >> 23) - 127 - 11);
+    const float2 m0 = __bfloat1622float2(__hmax2(most[0], most[1]));
+    const float top = fmaxf(m0.x, m0.y);
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 t = __bfloat1622float2(sums[k]);
+      sum += t.x + t.y;
+    }
+    // largest magnitude to (224, 448], with an outlier to [2^11, 2^12)
+    const bool outlier = top + top > sum;
+    const uint32_t tb = __float_as_uint(top);
+    const int less = outlier ? 11 : 8 - ((tb & 0x7fffffu) > 0x600000u);
+    const int e = max(-100, (int)(tb >> 23) - 127 - less);
     const float down = exp2_int(-e);
-    // what e5m2 has to take of a number beyond e4m3's largest
-    auto beyond = [](float a, float code) -> float {
-      return fabsf(a) > 448.f ? code : 0.f;
-    };
     // codes have no infinity: a row that holds one has scores that are not
     // numbers
     const float f = isinf(top) ? top - top : exp2_int(e) * kQScale;
+    // what lo has to take first of a number beyond hi's largest: its nearest
+    // number of 3 bits
+    auto beyond = [](float a) -> float {
+      const uint32_t near = __float_as_uint(a) + 0x100000u;
+      return fabsf(a) > 448.f ? __uint_as_float(near & 0xffe00000u) : 0.f;
+    };
+    auto codes = [&](auto first) {
 #pragma unroll 2
-    for (int i = 0; i < 8; ++i) {  // 16 dims
-      uint32_t hi[4], lo[4];
+      for (int i = 0; i < 8; ++i) {  // 16 dims
+        uint32_t hi[4], lo[4];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const uint4 v =
-            in ? __ldg(src + 2 * i + k) : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+        for (int k = 0; k < 2; ++k) {
+          const uint4 v =
+              in ? __ldg(src + 2 * i + k) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int n2 = 0; n2 < 2; ++n2) {
-          const float a0 = bf16_lo(x[2 * n2]) * down;
-          const float a1 = bf16_hi(x[2 * n2]) * down;
-          const float a2 = bf16_lo(x[2 * n2 + 1]) * down;
-          const float a3 = bf16_hi(x[2 * n2 + 1]) * down;
-          const float2 b0 = e5m2x2_to(e5m2x2_from(a0, a1));
-          const float2 b1 = e5m2x2_to(e5m2x2_from(a2, a3));
-          const uint32_t c =
-              e4m3x2_from(a0 - beyond(a0, b0.x), a1 - beyond(a1, b0.y)) |
-              e4m3x2_from(a2 - beyond(a2, b1.x), a3 - beyond(a3, b1.y)) << 16;
-          const float2 h0 = __half22float2(u32_as_h2(e4m3x2_lo(c)));
-          const float2 h1 = __half22float2(u32_as_h2(e4m3x2_hi(c)));
-          hi[2 * k + n2] = c;
-          lo[2 * k + n2] = e5m2x2_from(a0 - h0.x, a1 - h0.y) |
-                           e5m2x2_from(a2 - h1.x, a3 - h1.y) << 16;
+          for (int n2 = 0; n2 < 2; ++n2) {
+            const float a0 = bf16_lo(x[2 * n2]) * down;
+            const float a1 = bf16_hi(x[2 * n2]) * down;
+            const float a2 = bf16_lo(x[2 * n2 + 1]) * down;
+            const float a3 = bf16_hi(x[2 * n2 + 1]) * down;
+            const uint32_t c =
+                e4m3x2_from(a0 - first(a0), a1 - first(a1)) |
+                e4m3x2_from(a2 - first(a2), a3 - first(a3)) << 16;
+            const float2 h0 = __half22float2(u32_as_h2(e4m3x2_lo(c)));
+            const float2 h1 = __half22float2(u32_as_h2(e4m3x2_hi(c)));
+            hi[2 * k + n2] = c;
+            lo[2 * k + n2] = e5m2x2_from(a0 - h0.x, a1 - h0.y) |
+                             e5m2x2_from(a2 - h1.x, a3 - h1.y) << 16;
+          }
         }
+        const uint32_t at = q_s + tile * 2 * kPfQuery + (tid & 127) * 128 +
+                            ((i ^ (tid & 7)) << 4);
+        st_shared_v4(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+        st_shared_v4(at + kPfQuery, make_uint4(lo[0], lo[1], lo[2], lo[3]));
       }
-      const uint32_t at = q_s + tile * 2 * kPfQuery + (tid & 127) * 128 +
-                          ((i ^ (tid & 7)) << 4);
-      st_shared_v4(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-      st_shared_v4(at + kPfQuery, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-    }
+    };
+    if (__any_sync(0xffffffffu, outlier))
+      codes(beyond);
+    else
+      codes([](float) -> float { return 0.f; });
     fence_to_async();
     __syncwarp();
     if (lane == 0) mbar_arrive(sh.q_full + tile);
@@ -489,6 +516,7 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
     // rescales the sums in tensor memory
     auto rescale = [&](float fall) {
       tm_wait_st();
+#pragma unroll 1
       for (int k = 0; k < 8; ++k) {
         uint32_t o[16];
         tm_ld16(o, mine + kPfColO + 16 * k);
@@ -615,6 +643,7 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
             const float fall = raise(top, j > 0);
             tm_wait_st();
             // this tile's weights so far, rounded a second time
+#pragma unroll 1
             for (int k = 0; k < 2 * c; ++k) {
               uint32_t w[16];
               tm_ld16(w, mine + 16 * k);
