@@ -43,7 +43,7 @@
 // scores, in which the tensor core is busy with both row tiles for about 2,650
 // of 4,300.  The product of keys and query reads shared memory at 122 bytes a
 // cycle of 128 and runs at 70% of its rate.  A 128K prefix for 64 sequences and
-// 64 query heads takes 273 us in this form (300 with one row tile to a CTA);
+// 64 query heads takes 270 us in this form (300 with one row tile to a CTA);
 // with half of that product left out 24 us less, of the other 18, without the
 // exponentials 18, without the loads of key scales 19; without the stores of
 // widened values or of mended keys the same.  For few rows, the start and end
@@ -89,8 +89,8 @@ constexpr long long kPfMinShared = 12288;
 // A tile with value rows more than 2^kQSpread below the largest scale so far
 // takes its weights and values in bf16 (far_tile).  Twice the time, for tiles
 // after an outlier's alone: with an infinity in its first page a 128K prefix for
-// 64 sequences takes 511 us instead of 273 (the range that holds it is the last
-// to end), one of 32K for 32 48 us either way.
+// 64 sequences takes 502-508 us instead of 270 (the range that holds it is the
+// last to end), one of 32K for 32 47 us either way.
 
 // ---------------------------------------------------------------------------
 // tcgen05
@@ -661,7 +661,7 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
           // scores rounded before the reference is taken off, as it was: equal
           // ones stay equal and the largest differs from it by nothing, where a
           // difference rounded alone holds the reference's own rounding (at
-          // 10^11 up to 4096; 3 us of 273)
+          // 10^11 up to 4096; 3 us of 270)
           const float ref = kQLift - m;
           const uint64_t aa = pack2(ref, ref), zz = pack2(zero, zero);
 #pragma unroll
@@ -1060,14 +1060,14 @@ __global__ void __launch_bounds__(kPfThreads<R>, 3 - R)
 // 0 ranges: too little to share, every sequence reads the pages itself.
 // (Sequences, KV heads, pages, G = 4 unless given: read by each against once,
 // us, replayed back to back.)
-//   triples below the limit: 8, 8, 128: 12.2 and 14.6; 2, 8, 256: 10.8 and
-//     15.0; 32, 8, 32: 11.2 and 17.4; 64, 8, 16, G = 8: 15.6 and 18.5; 16, 8,
-//     64, G = 16: 13.9 and 21.8; 128, 1, 64, G = 8: 12.6 and 17.9; but 256, 8,
-//     4, G = 1: 23.5 and 18.5
-//   above: 8, 8, 256: 20.2 and 16.1; 2, 8, 1024: 20.2 and 21.8; 2, 8, 2048:
-//     27.7 and 29.1; 32, 8, 64: 22.1 and 17.8; 64, 8, 32, G = 8: 20.3 and 20.5;
-//     64, 8, 64, G = 8: 30.1 and 22.3; 16, 8, 128, G = 16: 26.6 and 22.0; 256, 8,
-//     8, G = 1: 27.1 and 18.6; 128, 1, 128, G = 8: 23.3 and 19.1
+//   triples below the limit: 8, 8, 128: 12.2 and 13.5; 2, 8, 256: 10.6 and
+//     13.9; 32, 8, 32: 11.1 and 16.2; 64, 8, 16, G = 8: 15.6 and 18.0; 16, 8,
+//     64, G = 16: 13.9 and 20.8; 128, 1, 64, G = 8: 12.5 and 16.6; but 256, 8,
+//     4, G = 1: 23.4 and 17.7
+//   above: 8, 8, 256: 20.4 and 15.0; 2, 8, 1024: 20.5 and 21.0; 2, 8, 2048:
+//     27.8 and 28.4; 32, 8, 64: 22.2 and 16.5; 64, 8, 32, G = 8: 20.3 and 20.1;
+//     64, 8, 64, G = 8: 30.1 and 20.9; 16, 8, 128, G = 16: 26.6 and 21.8; 256,
+//     8, 8, G = 1: 27.1 and 17.7; 128, 1, 128, G = 8: 23.4 and 18.0
 // One sequence shares nothing (1, 8, 8192: 64 and 77).  The numbers of SMs and
 // of CTAs that fit on them are this GPU's, written out.
 PrefixPlan prefix_plan(int batch, int h_kv, int G, int pages) {
