@@ -490,6 +490,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       // Beyond 2^24 a reference and a score's product with the scale differ by
       // more than the numbers nearby do: those rows go the plain way, as those
       // that a value that is no number could reach unseen.
+      // (m is 0 where there is no row)
       bool bad = fabsf(m) > kWinLargest && m > -INFINITY;
       uint32_t seen[2];  // tokens of a tile's half that the row sees
       bool whole = true;
@@ -674,8 +675,10 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       if (n > 0) ++units;
       // (weights up to 2^64 may have made large values' sums infinite)
       const bool again = my_row >= 0 && next > -INFINITY;
-      bad = my_row >= 0 && (bad || (large && l < INFINITY) ||
-                            (again && pass == kWinPasses));
+      // (a value that is no number has been met by the thread of its place, which
+      // may have no row)
+      bad |= (my_row >= 0 && large && l < INFINITY) ||
+             (again && pass == kWinPasses);
       if (any_of_tile(bad || again || !ok)) {
         if (any_of_tile(!ok)) break;
         if (any_of_tile(bad)) {
