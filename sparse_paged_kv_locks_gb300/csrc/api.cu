@@ -896,7 +896,7 @@ locks_status_t locks_window_attention(
        reinterpret_cast<float *>(ws + kWsHeader),
        reinterpret_cast<float2 *>(ws + kWsHeader +
                                   round_up(rows * kDim * 4, 256)),
-       0},
+       0, false},
       (cudaStream_t)stream);
   return e == cudaSuccess ? LOCKS_OK : fail_cuda(e);
 }

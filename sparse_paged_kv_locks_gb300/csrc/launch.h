@@ -175,7 +175,9 @@ struct WinArgs {
   int splits;       // ranges of each CTA's tiles
   float *o_part;    // [splits][n_tokens * h_q][128], sums not divided
   float2 *ml_part;  // [splits][n_tokens * h_q] (reference, sum of weights)
-  long long slots;  // (launch_window's)
+  // launch_window's: units, and whether outputs start at multiples of 32 bytes
+  long long slots;
+  bool wide;
 };
 cudaError_t launch_window(WinArgs a, cudaStream_t stream);
 // rules on sizes alone: the number of ranges, and rows of partials that no call

@@ -320,13 +320,20 @@ __device__ __forceinline__ uint32_t q_at(int r, int c) {
                     (((c & 7) ^ (r & 7)) << 4));
 }
 
-// a whole memory sector
-__device__ __forceinline__ void store32(void *to, const uint32_t *w) {
-  asm volatile(
-      "st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(to),
-      "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]),
-      "r"(w[6]), "r"(w[7])
-      : "memory");
+// 32 bytes: a whole memory sector where addresses allow it (`wide`; such a store
+// to another address is a fault), else 16 and 16
+__device__ __forceinline__ void store32(void *to, const uint32_t *w,
+                                        bool wide) {
+  if (wide)
+    asm volatile(
+        "st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(to),
+        "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]),
+        "r"(w[6]), "r"(w[7])
+        : "memory");
+  else
+    for (int i = 0; i < 2; ++i)
+      static_cast<uint4 *>(to)[i] =
+          make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
 }
 
 // Whether the values of a page of a unit's tile j take part in its product: of
@@ -653,15 +660,15 @@ __global__ void __launch_bounds__(kWinThreads, 1)
           const int at = 64 * half + 16 * c;
           if (a.splits > 1) {
             float *to = a.o_part + (split0 + my_row) * kDim + at;
-            store32(to, o);
-            store32(to + 8, o + 8);
+            store32(to, o, a.wide);
+            store32(to + 8, o + 8, a.wide);
           } else {
             uint32_t w[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               w[i] = pack_bf16(__uint_as_float(o[2 * i]) * inv,
                                __uint_as_float(o[2 * i + 1]) * inv);
-            store32(a.o + (size_t)my_row * kDim + at, w);
+            store32(a.o + (size_t)my_row * kDim + at, w, a.wide);
           }
         }
         __syncwarp();
@@ -1127,6 +1134,9 @@ cudaError_t launch_window(WinArgs a, cudaStream_t stream) {
       !cache_map(a, a.v, &v_map))
     return cudaErrorInvalidValue;
   a.slots = window_slots(a.n_tokens, a.batch, a.G);
+  // what the softmax's warps write to, rows of 256 or 512 bytes
+  a.wide = reinterpret_cast<uintptr_t>(
+               a.splits > 1 ? static_cast<void *>(a.o_part) : a.o) % 32 == 0;
   const long long base = a.slots * a.h_kv;
   e = launch_pdl(window_kernel, dim3((unsigned)(base * a.splits)),
                  dim3(kWinThreads), kWinSmem, stream, a, q_map, k_map,
