@@ -191,60 +191,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// A row tile's rows over tiles [j0, j1) in the plainest way, a row to a warp
-// (`w` of eight) and a token at a time: tokens that a row does not see are not
-// touched for it.
-__device__ __noinline__ void plain_rows(const WinArgs &a, const WinRows &r,
-                                        int h, int j0, int j1, int split,
-                                        int tile, int w) {
-  const int lane = threadIdx.x & 31, T = tile_tokens(a.G);
-  const int end = min((tile + 1) * T, r.tokens) * a.G;
-  for (int i = tile * T * a.G + w; i < end; i += 8) {
-    const int p = r.p0 + i / a.G;
-    const size_t row = out_row(a, r, h, i / a.G, i % a.G);
-    const uint2 qw = reinterpret_cast<const uint2 *>(a.q + row * kDim)[lane];
-    float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int j = j0; j < j1; ++j)
-      for (int t = r.tile(j) * kWinTile;
-           t < (r.tile(j) + 1) * kWinTile && t <= p; ++t) {
-        if (t >= a.sinks && t <= p - a.window) continue;
-        const int ph = __ldg(a.pt + (size_t)r.b * a.max_pages + t / kPage);
-        if (ph < 0 || ph >= a.num_phys) continue;
-        const size_t at =
-            (((size_t)ph * a.h_kv + h) * kPage + t % kPage) * kDim;
-        const uint2 k = reinterpret_cast<const uint2 *>(a.k + at)[lane];
-        float x = bf16_lo(qw.x) * bf16_lo(k.x) + bf16_hi(qw.x) * bf16_hi(k.x) +
-                  bf16_lo(qw.y) * bf16_lo(k.y) + bf16_hi(qw.y) * bf16_hi(k.y);
-#pragma unroll
-        for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-        const float top = fmaxf(m, x), ref = top == -INFINITY ? 0.f : top;
-        const float c = exp2f((m - ref) * kWinScale);
-        const float w = exp2f((x - ref) * kWinScale);
-        m = top;
-        const uint2 v = reinterpret_cast<const uint2 *>(a.v + at)[lane];
-        l = l * c + w;
-        o[0] = o[0] * c + w * bf16_lo(v.x);
-        o[1] = o[1] * c + w * bf16_hi(v.x);
-        o[2] = o[2] * c + w * bf16_lo(v.y);
-        o[3] = o[3] * c + w * bf16_hi(v.y);
-      }
-    if (a.splits > 1) {
-      const size_t part = (size_t)split * a.n_tokens * a.h_kv * a.G + row;
-      reinterpret_cast<float4 *>(a.o_part + part * kDim)[lane] =
-          make_float4(o[0], o[1], o[2], o[3]);
-      if (lane == 0) a.ml_part[part] = make_float2(m * kWinScale, l);
-      continue;
-    }
-    const float inv = l != 0.f ? 1.f / l : 0.f;
-    reinterpret_cast<uint2 *>(a.o + row * kDim)[lane] =
-        make_uint2(pack_bf16(o[0] * inv, o[1] * inv),
-                   pack_bf16(o[2] * inv, o[3] * inv));
-    if (lane == 0)
-      a.lse[row] =
-          l != 0.f ? (m * kWinScale + log2f(l)) * kWinLn2 : -INFINITY;
-  }
-}
-
 // What a CTA works on at a time: rows of a (sequence, KV head), the row tiles of
 // them (bits), and a range of their tiles.
 struct WinUnit {
@@ -258,6 +204,7 @@ struct WinShared {
   WinUnit unit[2];
   uint32_t tmem, there[4];  // which pages of tile j are there, at j & 3
   int dead;
+  uint32_t moved;  // when the CTA was last seen to move (win_wait)
   float other[2][2][kWinRows];  // what the halves of a row tell each other
   // of a unit's place; of a row tile; of a buffer; of `there`
   uint64_t unit_full[2], unit_free[2];
@@ -268,19 +215,166 @@ struct WinShared {
 
 static_assert(sizeof(WinShared) <= kWinHeader, "shared memory");
 
-// false when the wait gave up, or some other thread's did
+// Time on an SM in 2^16 cycles, and the CTA's sign that it moves.
+__device__ __forceinline__ uint32_t win_time() {
+  return (uint32_t)(clock64() >> 16);
+}
+__device__ __forceinline__ void win_moves(WinShared &sh) {
+  *(volatile uint32_t *)&sh.moved = win_time();
+}
+
+// False when the wait gave up, or some other thread's did.  The copies' warp, whose
+// waits end with the tiles and with the units before, gives up after some time in
+// which no tile was taken up in the plain way either.  The others may wait for as
+// long as a unit takes, whose tiles are not theirs or in that way; they leave it to
+// the copies' warp, which has a wait of its own until the last unit's end, and to a
+// limit beyond any unit (2^30 tokens in the plain way take some 2^43 cycles).  (The
+// same look at `moved` in the softmax's waits: eight ragged prompts 137 us instead
+// of 129.)
+constexpr long long kWinUnitCycles = 1LL << 45;
+template <bool COPIES = false>
 __device__ __forceinline__ bool win_wait(WinShared &sh, uint64_t *bar,
                                          uint32_t phase) {
   if (mbar_try_wait(bar, phase)) return true;
   const long long t0 = clock64();
   while (!*(volatile int *)&sh.dead) {
     if (mbar_try_wait(bar, phase)) return true;
-    if (clock64() - t0 > kQWaitCycles) {
+    const long long t = clock64();
+    // (a move may be later than the clock that was read)
+    if (COPIES ? t - t0 > kQWaitCycles &&
+                     (int)((uint32_t)(t >> 16) -
+                           *(volatile uint32_t *)&sh.moved) >
+                         (int)(kQWaitCycles >> 16)
+               : t - t0 > kWinUnitCycles) {
       *(volatile int *)&sh.dead = 1;
       break;
     }
   }
   return false;
+}
+
+// The sums over a warp of kPlainTokens numbers a lane: that of x[i] in the lanes
+// whose upper bits are i.
+constexpr int kPlainTokens = 8;
+__device__ __forceinline__ float sum_of_each(float (&x)[kPlainTokens]) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kSame = 32 / kPlainTokens;  // lanes that end with the same sum
+#pragma unroll
+  for (int n = kPlainTokens / 2; n; n >>= 1) {  // n sums each
+    const bool up = lane & kSame * n;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float other =
+          __shfl_xor_sync(0xffffffffu, up ? x[i] : x[i + n], kSame * n);
+      x[i] = (up ? x[i + n] : x[i]) + other;
+    }
+  }
+#pragma unroll
+  for (int d = kSame / 2; d; d >>= 1)
+    x[0] += __shfl_xor_sync(0xffffffffu, x[0], d);
+  return x[0];
+}
+
+// A row tile's rows over a unit's tiles in the plain way, a row to a warp, lane l
+// dims 4l .. 4l + 3, kPlainTokens tokens at a time: tokens that a row does not see
+// are not touched for it.  For 128 rows 2.0 us a token (65536 tokens 130 ms), 3.2
+// where keys and values come from memory (1M tokens 3.4 s), bound by the latency of
+// what eight warps load and exchange; a token at a time took 10.7.
+__device__ __noinline__ void plain_rows(const WinArgs &a, WinShared &sh, int u,
+                                        int tile) {
+  // (read where it is, again and again: the caller keeps its registers)
+  const volatile WinUnit &un = sh.unit[u & 1];
+  const int lane = threadIdx.x & 31;
+  constexpr int kSame = 32 / kPlainTokens;
+  int i = tile * tile_tokens(a.G) * a.G + (threadIdx.x >> 5 & 7);
+  for (; i < min((tile + 1) * tile_tokens(a.G), un.r.tokens) * a.G; i += 8) {
+    const int p = un.r.p0 + i / a.G;
+    const size_t row = (size_t)(un.r.q0 + i / a.G) * (a.h_kv * a.G) +
+                       un.h * a.G + i % a.G;
+    const uint2 q = reinterpret_cast<const uint2 *>(a.q + row * kDim)[lane];
+    // l: of the tokens whose number mod kPlainTokens is lane / kSame
+    float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int j = un.j0; j < un.j0 + un.n; ++j) {
+      if (lane == 0) win_moves(sh);
+      const int first = (j < un.r.head ? j : un.r.from + j - un.r.head) * kWinTile;
+      const int end = min(p + 1, first + kWinTile);
+      int ids = -1;  // of the tile's pages, a lane each
+      if (lane < kWinPages && first + lane * kPage < end)
+        ids = __ldg(a.pt + (size_t)un.r.b * a.max_pages + first / kPage + lane);
+#pragma unroll 1
+      for (int t0 = first; t0 < end; t0 += kPlainTokens) {
+        const int ph =
+            __shfl_sync(0xffffffffu, ids, (t0 - first) / kPage);
+        if (ph < 0 || ph >= a.num_phys) continue;
+        auto sees = [&](int t) -> bool {
+          return t <= p && (t < a.sinks || t > p - a.window);
+        };
+        const bool my_token = sees(t0 + lane / kSame);
+        const uint32_t seen = __ballot_sync(0xffffffffu, my_token);
+        if (seen == 0) continue;
+        const size_t at =
+            ((((size_t)ph * a.h_kv + un.h) * kPage + t0 % kPage) * kDim) / 4 +
+            lane;
+        uint2 v[kPlainTokens];
+        auto load = [&](const __nv_bfloat16 *cache) {
+          const uint2 *from = reinterpret_cast<const uint2 *>(cache) + at;
+#pragma unroll
+          for (int u = 0; u < kPlainTokens; ++u)
+            v[u] = seen >> kSame * u & 1 ? from[u * (kDim / 4)]
+                                         : make_uint2(0u, 0u);
+        };
+        load(a.k);
+        float part[kPlainTokens];
+#pragma unroll
+        for (int u = 0; u < kPlainTokens; ++u)
+          part[u] = bf16_lo(q.x) * bf16_lo(v[u].x) +
+                    bf16_hi(q.x) * bf16_hi(v[u].x) +
+                    bf16_lo(q.y) * bf16_lo(v[u].y) +
+                    bf16_hi(q.y) * bf16_hi(v[u].y);
+        asm volatile("" ::: "memory");
+        load(a.v);  // under the sums and exponentials
+        float x = sum_of_each(part);
+        if (!my_token) x = -INFINITY;
+        float top = fmaxf(m, x);
+#pragma unroll
+        for (int d = kSame; d < 32; d <<= 1)
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const float ref = top == -INFINITY ? 0.f : top;
+        const float c = exp2f((m - ref) * kWinScale);
+        const float weight = exp2f((x - ref) * kWinScale);
+        m = top;
+        l = l * c + weight;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) o[d] *= c;
+#pragma unroll
+        for (int u = 0; u < kPlainTokens; ++u) {
+          const float wu = __shfl_sync(0xffffffffu, weight, kSame * u);
+          o[0] += wu * bf16_lo(v[u].x);
+          o[1] += wu * bf16_hi(v[u].x);
+          o[2] += wu * bf16_lo(v[u].y);
+          o[3] += wu * bf16_hi(v[u].y);
+        }
+      }
+    }
+#pragma unroll
+    for (int d = kSame; d < 32; d <<= 1)
+      l += __shfl_xor_sync(0xffffffffu, l, d);
+    if (a.splits > 1) {
+      const size_t part = (size_t)un.split * a.n_tokens * a.h_kv * a.G + row;
+      reinterpret_cast<float4 *>(a.o_part + part * kDim)[lane] =
+          make_float4(o[0], o[1], o[2], o[3]);
+      if (lane == 0) a.ml_part[part] = make_float2(m * kWinScale, l);
+      continue;
+    }
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    reinterpret_cast<uint2 *>(a.o + row * kDim)[lane] =
+        make_uint2(pack_bf16(o[0] * inv, o[1] * inv),
+                   pack_bf16(o[2] * inv, o[3] * inv));
+    if (lane == 0)
+      a.lse[row] =
+          l != 0.f ? (m * kWinScale + log2f(l)) * kWinLn2 : -INFINITY;
+  }
 }
 
 // A page's 16 rows of one head, 4 KB, to [8-row group][64 dims][row][128 bytes]:
@@ -406,6 +500,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     mbar_init(&sh.answered, 1);
     mbar_init(&sh.drain, 1);
     sh.dead = 0;
+    win_moves(sh);
     fence_mbar_init();
   }
   __syncwarp();
@@ -689,7 +784,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       if (any_of_tile(bad || again || !ok)) {
         if (any_of_tile(!ok)) break;
         if (any_of_tile(bad)) {
-          plain_rows(a, r, un.h, j0, j0 + n, un.split, tile, wid & 7);
+          plain_rows(a, sh, u, tile);
         } else {
           // (a row that asks for nothing keeps the reference that it has)
           const float both = fmaxf(fmaxf(m, next), others(next));
@@ -798,7 +893,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     int asks = 0;
     // a unit's place is free; what it wants again
     auto collect = [&](int u) {
-      ok = win_wait(sh, sh.unit_free + (u & 1), u >> 1 & 1);
+      ok = win_wait<true>(sh, sh.unit_free + (u & 1), u >> 1 & 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
       WinUnit &un = sh.unit[u & 1];
@@ -827,7 +922,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         } else if (more) {
           if (!asked && lane == 0) ask(sh);
           asked = false;
-          ok = win_wait(sh, &sh.answered, asks++ & 1);
+          ok = win_wait<true>(sh, &sh.answered, asks++ & 1);
           ok = __all_sync(0xffffffffu, ok);
           id = answer(sh);
           // (read before the next answer is written there)
@@ -894,7 +989,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         for (int kv = 0; kv < 2; ++kv, ++s) {
           const int b = s % kWinStages;
           if (s >= kWinStages)
-            ok = win_wait(sh, sh.free + b, (s / kWinStages - 1) & 1);
+            ok = win_wait<true>(sh, sh.free + b, (s / kWinStages - 1) & 1);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           if (lane == 0) mbar_arrive_tx(sh.full + b, __popc(there) * kWinPage);
@@ -910,7 +1005,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
           for (int t = 0; t < 2; ++t) {
             if (!(un.mask >> t & 1)) continue;
             if (queries[t] > 0)
-              ok = win_wait(sh, sh.q_free + t, (queries[t] - 1) & 1);
+              ok = win_wait<true>(sh, sh.q_free + t, (queries[t] - 1) & 1);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             ++queries[t];
