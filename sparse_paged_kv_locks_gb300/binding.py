@@ -709,6 +709,27 @@ class Rotation:
                    amplitude, None if sections is None else len(sections))
 
 
+def _req_rotary(index, t, rotation, n, what):
+    """Positions [n_axes][n] (of one axis: also [n]): by their shape, since
+    [n][n_axes] has as many numbers, in another order."""
+    _req_on(index, t, "rotary_positions", torch.int32)
+    if t.shape != (rotation.n_axes, n) and \
+            not (rotation.n_axes == 1 and t.shape == (n,)):
+        raise ValueError(f"rotary_positions must be [n_axes][{what}]")
+
+
+def _req_turning(index, rotation, rotary_positions, append, batch):
+    """A decoder's rotation, checked."""
+    if rotation is None:
+        return
+    if not append:
+        raise ValueError("a rotation needs append=True")
+    if not isinstance(rotation, Rotation):
+        raise TypeError("rotation must be a Rotation")
+    if rotary_positions is not None:
+        _req_rotary(index, rotary_positions, rotation, batch, "batch")
+
+
 def _req_rotate(q, k_new, v_new, rotation, rotary_positions, seq_ids,
                 positions, page_table, q_out, h_kv, index, status):
     """The leading arguments of the two calls, checked."""
@@ -732,9 +753,7 @@ def _req_rotate(q, k_new, v_new, rotation, rotary_positions, seq_ids,
         if q_out.shape != q.shape:
             raise ValueError("q_out must be [n][h_q][128]")
     if rotary_positions is not None:
-        _req_on(index, rotary_positions, "rotary_positions", torch.int32)
-        if rotary_positions.numel() != rotation.n_axes * n:
-            raise ValueError("rotary_positions must be [n_axes][n]")
+        _req_rotary(index, rotary_positions, rotation, n, "n")
     if status is not None:
         _req_on(index, status, "status", torch.int32)
     return (_addr(q), k_new.data_ptr(), v_new.data_ptr(),
@@ -821,9 +840,7 @@ def locks_append_rotated_kv(q, k_new, v_new, rotation, q_out, k_cache,
         raise ValueError("summaries must be [batch][h_kv][max_pages][832], "
                          "seq_lens [batch]")
     if rotary_positions is not None:
-        _req_on(index, rotary_positions, "rotary_positions", torch.int32)
-        if rotary_positions.numel() != rotation.n_axes * batch:
-            raise ValueError("rotary_positions must be [n_axes][batch]")
+        _req_rotary(index, rotary_positions, rotation, batch, "batch")
     if tau_out is not None:
         _req_on(index, tau_out, "tau_out", torch.float32)
         if tau_out.numel() < batch * h_kv:
@@ -1005,8 +1022,8 @@ class LocksDecoder:
             self.k_new = torch.empty(self.batch, self.h_kv, HEAD_DIM,
                                      dtype=torch.bfloat16, device=dev)
             self.v_new = torch.empty_like(self.k_new)
-        elif rotation is not None:
-            raise ValueError("a rotation needs append=True")
+        _req_turning(k_cache.get_device(), rotation, rotary_positions, append,
+                     self.batch)
         self.rotation, self.rotary_positions = rotation, rotary_positions
         if rotation is not None:
             self.q_turned = torch.empty_like(self.q_dev)

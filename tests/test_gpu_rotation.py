@@ -390,3 +390,37 @@ def test_other_stream_and_graph():
     assert torch.equal(a.kc, b.kc)
     near_bf16(num(b.qo), W.rotate(num(b.q), [b.pos], frequencies(128)),
               W.rotate_reach(num(b.q), frequencies(128)))
+
+
+def test_positions_in_another_order_are_refused():
+    """[n][n_axes] instead of [n_axes][n], by all calls and the decoder."""
+    c = Case(2, [20, 3], 8, 2)
+    rot = B.Rotation(frequencies(128), axes=[j % 3 for j in range(64)])
+    wrong = np.zeros((c.n, 3), np.int32)
+    for call in (c.bf16, c.e4m3):
+        with pytest.raises(ValueError, match="n_axes"):
+            call(rot, wrong)
+    assert (c.kc == 7.0).all() and (c.rec == 171).all() and (c.qo == 5.0).all()
+    lens, q = i32([3, 4]), torch.ones(2, 8, 128, dtype=torch.bfloat16,
+                                      device=DEV)
+    store = B.new_summary_store(2, 2, c.pages)
+    with pytest.raises(ValueError, match="n_axes"):
+        B.locks_append_rotated_kv(q, q[:, :2].contiguous(),
+                                  q[:, :2].contiguous(), rot, q, c.kc, c.vc,
+                                  i32(c.table), lens, store,
+                                  rotary_positions=i32(wrong[:2]))
+    assert lens.tolist() == [3, 4] and (c.kc == 7.0).all()
+
+    def decoder(**kw):
+        return B.LocksDecoder(c.kc, c.vc, i32(c.table), store, 8, 1,
+                              seq_lens=lens, **kw)
+
+    for kw in ({"rotation": rot, "rotary_positions": i32(wrong[:2])},
+               {"rotation": rot, "rotary_positions": i32(wrong[:3].T.copy())}):
+        with pytest.raises(ValueError):
+            decoder(append=True, **kw)
+    with pytest.raises(ValueError):
+        decoder(rotation=rot)
+    with pytest.raises(TypeError):
+        decoder(append=True, rotation=frequencies(128))
+    decoder(append=True, rotation=rot, rotary_positions=i32(np.zeros((3, 2))))

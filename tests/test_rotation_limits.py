@@ -144,3 +144,37 @@ def test_binding_refuses_cpu_tensors(L):
         B.locks_append_rotated_kv(k, k, k, rot, k, kc, kc, t, i,
                                   torch.zeros(1, 2, 4, 832,
                                               dtype=torch.uint8))
+
+
+def test_positions_are_checked_by_their_shape(L):
+    """[n][n_axes], which has as many numbers as [n_axes][n], is refused.  (On
+    the CPU, whose tensors are on GPU -1.)"""
+    import torch
+    three = B.Rotation([1.0] * 9 + [0.5] * 7, axes=[0] * 4 + [1] * 6 + [2] * 6)
+    one = B.Rotation([1.0] * 8)
+
+    def ints(*shape):
+        return torch.zeros(*shape, dtype=torch.int32)
+
+    for rot, t in ((three, ints(3, 5)), (one, ints(1, 5)), (one, ints(5))):
+        B._req_rotary(-1, t, rot, 5, "n")
+        B._req_turning(-1, rot, t, True, 5)
+    for rot, t in ((three, ints(5, 3)), (three, ints(15)), (one, ints(5, 1)),
+                   (three, ints(1, 5)), (one, ints(3, 5)), (one, ints(4)),
+                   (three, ints(5, 3).t()), (one, ints(1, 10)[:, ::2])):
+        with pytest.raises(ValueError):
+            B._req_rotary(-1, t, rot, 5, "n")
+        with pytest.raises(ValueError):
+            B._req_turning(-1, rot, t, True, 5)
+    with pytest.raises(TypeError):
+        B._req_turning(-1, three, ints(3, 5).long(), True, 5)
+
+
+def test_a_decoder_checks_its_rotation_at_once(L):
+    rot = B.Rotation([1.0] * 8)
+    B._req_turning(-1, None, None, False, 5)
+    B._req_turning(-1, rot, None, True, 5)
+    with pytest.raises(TypeError):
+        B._req_turning(-1, [1.0] * 8, None, True, 5)
+    with pytest.raises(ValueError):
+        B._req_turning(-1, rot, None, False, 5)
