@@ -390,7 +390,7 @@ locks_status_t locks_sparse_decode(
  * notes §2, Fig. 1): token position L = seq_lens[b] is written to page
  * L/16 slot L%16 for every KV head, then, if (L+1) % 16 == 0, the record of
  * that page is built as in locks_build_summaries; seq_lens[b] becomes L+1.
- *   k_new, v_new  bf16 [batch][h_kv][128]
+ *   k_new, v_new  bf16 [batch][h_kv][128], 8-byte aligned, as the caches are
  *   seq_lens      int32 [batch], updated in place on the device
  *   tau_out       optional float [batch][h_kv] (written for built pages) */
 locks_status_t locks_append_kv(const void *k_new, const void *v_new,

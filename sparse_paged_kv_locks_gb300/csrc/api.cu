@@ -4,6 +4,8 @@
 #include <math.h>
 #include <stdio.h>
 
+#include <initializer_list>
+
 #include "common.cuh"
 #include "launch.h"
 
@@ -421,6 +423,19 @@ locks_status_t locks_append_kv(const void *k_new, const void *v_new,
                             summaries, tau_out, 0, status, stream);
 }
 
+static bool aligned16(const void *p) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
+}
+
+// what an append loads and stores: 8 bytes a lane of a row, 16 of a record
+static bool append_aligned(const void *k_new, const void *v_new,
+                           const void *k_cache, const void *v_cache,
+                           const void *summaries) {
+  for (const void *p : {k_new, v_new, k_cache, v_cache})
+    if (reinterpret_cast<uintptr_t>(p) & 7u) return false;
+  return aligned16(summaries);
+}
+
 locks_status_t locks_append_kv_ex(const void *k_new, const void *v_new,
                                   void *k_cache, void *v_cache,
                                   int64_t num_phys_pages, int h_kv,
@@ -434,7 +449,7 @@ locks_status_t locks_append_kv_ex(const void *k_new, const void *v_new,
   if (h_kv > 32) return LOCKS_ERR_UNSUPPORTED;
   if (batch == 0) return LOCKS_OK;
   if (!k_new || !v_new || !k_cache || !v_cache || !page_table || !seq_lens ||
-      !summaries)
+      !summaries || !append_aligned(k_new, v_new, k_cache, v_cache, summaries))
     return LOCKS_ERR_INVALID_ARG;
   cudaError_t e = launch_append(k_new, v_new, k_cache, v_cache, num_phys_pages,
                                 h_kv, page_table, batch, max_pages, seq_lens,
@@ -446,10 +461,6 @@ locks_status_t locks_append_kv_ex(const void *k_new, const void *v_new,
 // ---------------------------------------------------------------------------
 // quantised KV cache
 // ---------------------------------------------------------------------------
-static bool aligned16(const void *p) {
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
-}
-
 static bool type_ok(int type) {
   return type == LOCKS_TYPE_BF16 || type == LOCKS_TYPE_FP16 ||
          type == LOCKS_TYPE_FP32;
@@ -759,7 +770,9 @@ locks_status_t locks_append_rotated_kv(
   if (!q || !q_out || !k_new || !v_new || !k_cache || !v_cache ||
       !page_table || !seq_lens || !summaries)
     return LOCKS_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(q_out)) return LOCKS_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(q_out) ||
+      !append_aligned(k_new, v_new, k_cache, v_cache, summaries))
+    return LOCKS_ERR_INVALID_ARG;
   cudaError_t e = launch_append_rotated(
       {q, q_out, h_q, rotary_positions, *rotation}, k_new, v_new, k_cache,
       v_cache, num_phys_pages, h_kv, page_table, batch, max_pages, seq_lens,

@@ -178,3 +178,22 @@ def test_a_decoder_checks_its_rotation_at_once(L):
         B._req_turning(-1, [1.0] * 8, None, True, 5)
     with pytest.raises(ValueError):
         B._req_turning(-1, rot, None, False, 5)
+
+
+def test_append_refuses_rows_that_it_cannot_load(L):
+    """Eight bytes a lane of keys, values and caches, sixteen of records, with
+    a rotation and without."""
+    off4, off8 = ctypes.c_void_p((1 << 12) + 4), ODD
+    rot = B.Rotation([1.0] * 64)._at
+    turned = [FAKE, FAKE, FAKE, rot, None, 8, FAKE, FAKE, FAKE, 10, 2, FAKE,
+              0, 16, FAKE, FAKE, None, 0, None, None]
+    plain = [FAKE, FAKE, FAKE, FAKE, 10, 2, FAKE, 0, 16, FAKE, FAKE, None, 0,
+             None, None]
+    for call, good, rows, batch, records in (
+            (L.locks_append_rotated_kv, turned, (1, 2, 7, 8), 12, 15),
+            (L.locks_append_kv_ex, plain, (0, 1, 2, 3), 7, 10)):
+        assert call(*good) == 0            # a batch of none
+        for i, bad in [(i, off4) for i in rows] + [(records, off8)]:
+            args = list(good)
+            args[batch], args[i] = 1, bad
+            assert call(*args) == 1, i
