@@ -154,3 +154,55 @@ def test_binding_refuses_what_int32_does_not_hold(L, window, sinks):
         B.locks_window_workspace_size(1, 1, 1, 1, 1, window, sinks)
     assert B.locks_window_workspace_size(1, 1, 1, 1, 1, B.EVERY_TOKEN,
                                          B.EVERY_TOKEN) > 0
+
+
+def ranges(n, batch, h_kv, G, pages, window, sinks):
+    """The number of ranges that a call cuts each unit's tiles into, stated
+    apart from the library: the least estimate of rounds of units, each of its
+    tiles, its start and end, and of joining."""
+    tokens = 2 * (128 // G)
+    window, sinks = min(window, 16 * pages), min(sinks, 16 * pages)
+    tiles = min((min(tokens, n) + window + 126) // 128 + 1 +
+                (sinks + 127) // 128, (16 * pages + 127) // 128)
+    units = max(-(-n // tokens), batch) * h_kv
+    rows = n * h_kv * G
+    best, cost = 1, None
+    for s in range(1, min(64, tiles) + 1):
+        if s > 1 and rows * s > 65536:
+            break
+        c = -(-units * s // 152) * (-(-tiles // s) + 3.5)
+        if s > 1:
+            c += 3.0 + 1.2e-4 * (rows * s)
+        if cost is None or c < cost:
+            best, cost = s, c
+    return best
+
+
+def test_a_call_needs_no_more_than_the_size_reported(L):
+    """Of one byte less than its own ranges' partials a call is refused, and
+    that is within the size reported, for sizes on every side of the rules.
+    (Where there is no GPU, so that a call which is not refused ends there.)"""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("the calls' pointers are not memory")
+    seen = set()
+    for n in (1, 4, 17, 64, 65, 300, 5000):
+        for batch in (1, 2, 16, 130):
+            for h_kv, G in ((8, 4), (1, 16), (2, 5)):
+                for pages in (1, 9, 150, 2000, 30000):
+                    for window, sinks in ((1, 0), (300, 5), (5000, 200),
+                                          (2 ** 31 - 1, 0)):
+                        s = ranges(n, batch, h_kv, G, pages, window, sinks)
+                        seen.add(s)
+                        rows = s * n * h_kv * G if s > 1 else 0
+                        own = 256 + rows * 512 + -(-rows * 8 // 256) * 256
+                        need = size(n, batch, h_kv * G, h_kv, pages, window,
+                                    sinks)
+                        assert own <= need
+                        a = {**GOOD, "n": n, "batch": batch, "h_kv": h_kv,
+                             "h_q": h_kv * G, "pages": pages,
+                             "window": window, "sinks": sinks,
+                             "bytes": own - 1}
+                        assert L.locks_window_attention(
+                            *[a[x] for x in CHUNK]) == 3, (a, s)
+    assert len(seen) > 20
