@@ -186,7 +186,7 @@ def test_a_call_needs_no_more_than_the_size_reported(L):
     if torch.cuda.is_available():
         pytest.skip("the calls' pointers are not memory")
     seen = set()
-    for n in (1, 4, 17, 64, 65, 300, 5000):
+    for n in (1, 4, 17, 64, 65, 300, 1365, 5000):
         for batch in (1, 2, 16, 130):
             for h_kv, G in ((8, 4), (1, 16), (2, 5)):
                 for pages in (1, 9, 150, 2000, 30000):
