@@ -1060,13 +1060,15 @@ class LocksDecoder:
         side = torch.cuda.Stream()
         side.wait_stream(cur)
         with torch.cuda.stream(side):   # one-time setup outside the capture
+            before = self.seq_lens_dev.clone() if self.append else None
             self._eager(self.q_dev, self.seq_lens_dev, None, self.k_new_b,
                         self.v_new_b)
             if self.append:
                 # the warm-up appended this step's token; the replay that
                 # follows writes it (and any page build) again at the same
-                # position, so the lengths go back by one
-                self.seq_lens_dev.sub_(1)
+                # position, so the lengths go back to what they were (those
+                # of sequences that took no token have not moved)
+                self.seq_lens_dev.copy_(before)
         cur.wait_stream(side)
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):

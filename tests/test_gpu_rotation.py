@@ -424,3 +424,40 @@ def test_positions_in_another_order_are_refused():
     with pytest.raises(TypeError):
         decoder(append=True, rotation=frequencies(128))
     decoder(append=True, rotation=rot, rotary_positions=i32(np.zeros((3, 2))))
+
+
+@pytest.mark.parametrize("turned", [False, True])
+def test_a_captured_append_leaves_a_full_sequence_alone(turned):
+    """A decoder's first captured step, like its eager one, appends to the
+    sequences that can take a token, and changes nothing of the others."""
+    rng = np.random.default_rng(4)
+    batch, h_q, h_kv, pages = 4, 8, 2, 3
+    lens = [48, 17, 31, 40]         # full; free; fills a page; a bad page
+    table = np.arange(batch * pages).reshape(batch, pages)
+    table[3, 2] = batch * pages
+    kc = torch.from_numpy(rng.standard_normal(
+        (batch * pages, h_kv, 16, 128))).to(torch.bfloat16).to(DEV)
+    vc = torch.randn_like(kc)
+    rows = [torch.from_numpy(rng.standard_normal((3, batch, h, 128))).to(
+        torch.bfloat16).to(DEV) for h in (h_q, h_kv, h_kv)]
+    kw = {"rotation": B.Rotation(frequencies(128))} if turned else {}
+
+    def decoder(graph):
+        d = B.LocksDecoder(kc.clone(), vc.clone(), i32(table),
+                           B.new_summary_store(batch, h_kv, pages), h_q, 2,
+                           seq_lens=i32(lens), append=True, graph=graph, **kw)
+        for q, k, v in zip(*rows):
+            d.step(q, k_new=k, v_new=v)
+        return d
+
+    eager, graph = decoder(False), decoder(True)
+    assert eager.seq_lens_dev.tolist() == [48, 20, 34, 40]
+    assert graph.seq_lens_dev.tolist() == [48, 20, 34, 40]
+    for d in (eager, graph):
+        assert torch.equal(d.k_cache[:3], kc[:3])
+        assert torch.equal(d.v_cache[:3], vc[:3])
+    assert torch.equal(graph.k_cache, eager.k_cache)
+    assert torch.equal(graph.v_cache, eager.v_cache)
+    assert torch.equal(graph.summaries, eager.summaries)
+    assert graph.status() == eager.status() == \
+        B.DEV_BAD_SEQ_LEN | B.DEV_BAD_PAGE_ID
