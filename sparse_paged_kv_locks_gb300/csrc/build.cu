@@ -736,14 +736,12 @@ struct NoRotation {};
 // One CTA per sequence, one warp per KV head.  With an AppendRotation the warp
 // turns its key and its group's queries on the way (rotate.cuh).
 template <class Rotation>
-__global__ void append_kernel(const __grid_constant__ Rotation ar,
-                              const __nv_bfloat16 *__restrict__ k_new,
-                              const __nv_bfloat16 *__restrict__ v_new,
-                              __nv_bfloat16 *k_cache, __nv_bfloat16 *v_cache,
-                              int64_t num_phys, int h_kv,
-                              const int32_t *__restrict__ pt, int max_pages,
-                              int32_t *seq_lens, uint8_t *summaries,
-                              float *tau_out, int flags, int32_t *status) {
+__device__ __forceinline__ void append_token(
+    const Rotation &ar, const __nv_bfloat16 *__restrict__ k_new,
+    const __nv_bfloat16 *__restrict__ v_new, __nv_bfloat16 *k_cache,
+    __nv_bfloat16 *v_cache, int64_t num_phys, int h_kv,
+    const int32_t *__restrict__ pt, int max_pages, int32_t *seq_lens,
+    uint8_t *summaries, float *tau_out, int flags, int32_t *status) {
   extern __shared__ __align__(16) unsigned char append_smem[];
   BuildSmem *smem = reinterpret_cast<BuildSmem *>(append_smem);
   const int b = blockIdx.x;
@@ -809,6 +807,34 @@ __global__ void append_kernel(const __grid_constant__ Rotation ar,
   }
   __syncthreads();
   if (threadIdx.x == 0 && ok) seq_lens[b] = pos + 1;
+}
+
+// A page's build wants 96 registers, which 20 warps can have at most; more KV heads
+// make do with 64 (without a rotation: with one there are 16 heads at most).
+constexpr int kAppendWarps = 20;
+template <class Rotation>
+__global__ void append_kernel(const __grid_constant__ Rotation ar,
+                              const __nv_bfloat16 *__restrict__ k_new,
+                              const __nv_bfloat16 *__restrict__ v_new,
+                              __nv_bfloat16 *k_cache, __nv_bfloat16 *v_cache,
+                              int64_t num_phys, int h_kv,
+                              const int32_t *__restrict__ pt, int max_pages,
+                              int32_t *seq_lens, uint8_t *summaries,
+                              float *tau_out, int flags, int32_t *status) {
+  append_token(ar, k_new, v_new, k_cache, v_cache, num_phys, h_kv, pt,
+               max_pages, seq_lens, summaries, tau_out, flags, status);
+}
+__global__ void __launch_bounds__(1024)
+    append_many_kernel(const __grid_constant__ NoRotation ar,
+                       const __nv_bfloat16 *__restrict__ k_new,
+                       const __nv_bfloat16 *__restrict__ v_new,
+                       __nv_bfloat16 *k_cache, __nv_bfloat16 *v_cache,
+                       int64_t num_phys, int h_kv,
+                       const int32_t *__restrict__ pt, int max_pages,
+                       int32_t *seq_lens, uint8_t *summaries, float *tau_out,
+                       int flags, int32_t *status) {
+  append_token(ar, k_new, v_new, k_cache, v_cache, num_phys, h_kv, pt,
+               max_pages, seq_lens, summaries, tau_out, flags, status);
 }
 
 // --------------------------------------------------------------------------
@@ -1036,12 +1062,19 @@ static cudaError_t append(const Rotation &turn, const void *k_new,
   const size_t smem = sizeof(BuildSmem) * (size_t)h_kv;
   static DeviceFlags attr_set;
   cudaError_t e = once_per_device(attr_set, [] {
-    return cudaFuncSetAttribute(append_kernel<Rotation>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)(sizeof(BuildSmem) * 32));
+    auto set = [](auto *kern) {
+      return cudaFuncSetAttribute(kern,
+                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  (int)(sizeof(BuildSmem) * 32));
+    };
+    const cudaError_t r = set(append_kernel<Rotation>);
+    return r == cudaSuccess ? set(append_many_kernel) : r;
   });
   if (e != cudaSuccess) return e;
-  append_kernel<<<batch, 32 * h_kv, smem, stream>>>(
+  auto *kern = append_kernel<Rotation>;
+  if constexpr (std::is_same_v<Rotation, NoRotation>)
+    if (h_kv > kAppendWarps) kern = append_many_kernel;
+  kern<<<batch, 32 * h_kv, smem, stream>>>(
       turn, static_cast<const __nv_bfloat16 *>(k_new),
       static_cast<const __nv_bfloat16 *>(v_new),
       static_cast<__nv_bfloat16 *>(k_cache),

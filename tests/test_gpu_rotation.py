@@ -461,3 +461,32 @@ def test_a_captured_append_leaves_a_full_sequence_alone(turned):
     assert torch.equal(graph.summaries, eager.summaries)
     assert graph.status() == eager.status() == \
         B.DEV_BAD_SEQ_LEN | B.DEV_BAD_PAGE_ID
+
+
+@pytest.mark.parametrize("h_kv", [1, 16, 20, 21, 22, 27, 32])
+def test_append_of_up_to_32_heads(h_kv):
+    """Every number of KV heads that the unrotated append takes: bytes of a
+    write by hand, summaries of a build of the whole page."""
+    rng = np.random.default_rng(h_kv)
+    lens, pages = [15, 3, 31], 2
+    table = i32(rng.permutation(6).reshape(3, 2))
+    kc = torch.from_numpy(rng.standard_normal((6, h_kv, 16, 128))).to(
+        torch.bfloat16).to(DEV)
+    vc = torch.randn_like(kc)
+    k, v = (torch.from_numpy(rng.standard_normal((3, h_kv, 128))).to(
+        torch.bfloat16).to(DEV) for _ in range(2))
+    want_k, want_v = kc.clone(), vc.clone()
+    for b, n in enumerate(lens):
+        want_k[table[b, n // 16].long(), :, n % 16] = k[b]
+        want_v[table[b, n // 16].long(), :, n % 16] = v[b]
+    seq, st = i32(lens), word()
+    store, tau = B.new_summary_store(3, h_kv, pages), torch.zeros(
+        3, h_kv, device=DEV)
+    B.locks_append_kv(k, v, kc, vc, table, seq, store, tau_out=tau, status=st)
+    assert int(st.item()) == 0 and seq.tolist() == [16, 4, 32]
+    assert torch.equal(kc, want_k) and torch.equal(vc, want_v)
+    built, tau2 = torch.zeros_like(store), torch.zeros(2, h_kv, device=DEV)
+    B.locks_build_summaries(kc, table, i32([0, 2]), i32([0, 1]), built,
+                            tau_out=tau2)
+    assert torch.equal(store, built) and built[0, :, 0].any(-1).all()
+    assert torch.equal(tau[[0, 2]], tau2)
