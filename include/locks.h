@@ -767,8 +767,14 @@ locks_status_t locks_window_decode(
  *   o_out     bf16 [n_tokens][h_q][128];  lse_out float [n_tokens][h_q]
  * Other arguments as locks_window_decode.  Status bits, besides its:
  * LOCKS_DEV_BAD_ROWS (the rows of a sequence whose starts descend or leave
- * 0 .. n_tokens are skipped).  LOCKS_ERR_UNSUPPORTED when n_tokens * h_q or
- * 16 * num_phys_pages * h_kv exceeds 2^31 - 1, or a table 2^30 tokens. */
+ * 0 .. n_tokens are skipped; where starts descend, rows of other sequences may
+ * be too).  LOCKS_ERR_UNSUPPORTED when n_tokens * h_q or
+ * 16 * num_phys_pages * h_kv exceeds 2^31 - 1, or a table 2^30 tokens.
+ *
+ * Rows of a token group (up to 128 rows of a KV head) take a slow way, some 2
+ * us a token that they see, where one of their scores is beyond 2^20 in base 2,
+ * where their sums pass fp32's range, or where a value that is no number is
+ * seen by some of the group's rows and not by others. */
 locks_status_t locks_window_attention(
     const void *q, const void *k_cache, const void *v_cache,
     int64_t num_phys_pages, const int32_t *page_table,

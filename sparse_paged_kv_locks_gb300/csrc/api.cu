@@ -765,6 +765,8 @@ locks_status_t locks_append_rotated_kv(
   if (!rotation_ok(rotation) || batch < 0 || !heads_ok(h_q, h_kv) ||
       max_pages < 1 || num_phys_pages < 1 || !build_flags_ok(flags))
     return LOCKS_ERR_INVALID_ARG;
+  // (a warp to a head: beyond 20 the append's form with 64 registers a thread would
+  // have to turn rows as well)
   if (h_kv > 16) return LOCKS_ERR_UNSUPPORTED;
   if (batch == 0) return LOCKS_OK;
   if (!q || !q_out || !k_new || !v_new || !k_cache || !v_cache ||

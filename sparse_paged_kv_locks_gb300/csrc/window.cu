@@ -23,17 +23,19 @@
 // Tiles that all rows see whole have no masks.  In the others a token that no
 // row sees has its value row cleared, whatever it holds, and a value that is
 // not finite, which a weight of zero would spread to rows that do not see it,
-// sends the row tile to the plain form (plain_rows), a token at a time.
+// sends the row tile to the plain form (plain_rows), in fp32, where a token that a
+// row does not see is not touched for it.
 //
 // Few rows over many tokens (drafted tokens, short parts of long prompts): the
 // tiles of a unit are cut into ranges, whose partials a second kernel joins.
 //
 // Bound: a prompt of 8192 tokens, 32 query and 8 KV heads, takes 343 us, 1600
-// TFLOP/s, a tile of both row tiles some 2,700 cycles: 2 * 684 for the scores
+// TFLOP/s, in bursts of a replayed graph (calls one after the other 366, 1503: the
+// board's power), a tile of both row tiles some 2,700 cycles: 2 * 684 for the scores
 // (64 in theory for each of 8 products of 16 dims; they read shared memory at all
 // of its 128 bytes a cycle and take 85), 2 * 533 for the weighted values, the
 // rest between them.  The tensor core is busy for 68% of the time, and the board
-// draws the 1,400 W that it may (1.9 GHz; in a loop of seconds 364 us).  A unit's
+// draws the 1,400 W that it may (1.9 GHz).  A unit's
 // start and end cost 9,000 cycles, the time of 3.5 tiles: 32768 tokens with a
 // window of 4096 (34 tiles a unit) 1345 to 1410 us, 1480 to 1550 TFLOP/s; eight
 // prompts of 100 to 2500 tokens and 5 heads to a group (6.5 tiles a unit) 128 us.
@@ -1185,7 +1187,9 @@ static int window_tiles(int n_tokens, int G, int max_pages, int window,
 // range 364 us, 2 to 6 ranges 372-377, 7 334, 8 338, 9 345, 12 358; 64 tokens
 // behind 2000, 8 units of 17 tiles: one 33, 3 22, 9 17.8; 1000 tokens behind 8000,
 // one KV head of 8 query heads: one 106, 3 49, 4 41, 5 58, since a fifth range
-// takes a second round.)
+// takes a second round.)  A sequence without rows counts as a unit too, which is far
+// off where few of many have some: 4 tokens of one sequence of 32K 35 us in a table
+// of one (19 ranges), 65 in a table of 16, 190 of 64, 358 of 128 (one range).
 int window_splits(int n_tokens, int batch, int h_kv, int G, int max_pages,
                   int window, int sinks) {
   const long long T2 = 2 * tile_tokens(G);
